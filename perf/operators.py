@@ -9,7 +9,7 @@ framework's entry points.
 
 Cache format (one layer): a block holds `bt` tokens; its bytes are records
 [kv head][unit of 16 tokens] of 544*nc bytes, nc = head_dim/32:
-  K codes [4 g][16 t][nc c][4 b]   nibbles: dims 32c+8g+2b (low), +1 (high) of token t
+  K codes [16 t][4 g][nc c][4 b]   nibbles: dims 32c+8g+2b (low), +1 (high) of token t
   V codes [4 g][16 d][nc c][4 j]   nibbles: dims 32c+d (low), 32c+16+d (high) of token 4g+j
   K scales [16 t][nc c], V scales [16 t][nc c]   2^(byte-127)
 Codes are sign, 2 exponent bits and 1 fraction bit: 0 .5 1 1.5 2 3 4 6.
@@ -335,8 +335,8 @@ def _plain_cache(s):
     rec = s["cache"][s["table"][:, :nb].clamp(min=0).long()].view(B, nb, H, U, 544 * nc)
     kc, vc, ks, vs = rec.split([256 * nc, 256 * nc, 16 * nc, 16 * nc], dim=-1)
     scale = lambda x: torch.ldexp(torch.ones((), device=DEV), x.int() - 127).view(B, nb, H, U, 16, nc)  # noqa: E731
-    k = _plain_values(torch.stack([kc & 15, kc >> 4], -1)).view(B, nb, H, U, 4, 16, nc, 4, 2)
-    k = k.permute(0, 1, 3, 5, 2, 6, 4, 7, 8).reshape(B, nb, U, 16, H, nc, 32) * scale(ks).permute(0, 1, 3, 4, 2, 5)[..., None]
+    k = _plain_values(torch.stack([kc & 15, kc >> 4], -1)).view(B, nb, H, U, 16, 4, nc, 4, 2)
+    k = k.permute(0, 1, 3, 4, 2, 6, 5, 7, 8).reshape(B, nb, U, 16, H, nc, 32) * scale(ks).permute(0, 1, 3, 4, 2, 5)[..., None]
     v = _plain_values(torch.stack([vc & 15, vc >> 4], -1)).view(B, nb, H, U, 4, 16, nc, 4, 2)
     v = v.permute(0, 1, 3, 4, 7, 2, 6, 8, 5).reshape(B, nb, U, 16, H, nc, 32) * scale(vs).permute(0, 1, 3, 4, 2, 5)[..., None]
     return k.reshape(B, nb * bt, H, D), v.reshape(B, nb * bt, H, D)
@@ -426,7 +426,7 @@ def exact(case, seed):
     bt, nc, H = case["bt"], D // 32, case["hkv"]
     t, d = torch.arange(16, device=DEV)[:, None], torch.arange(D, device=DEV)[None, :]
     c, r = d // 32, d % 32
-    k_at, k_high = (((r // 8) * 16 + t) * nc + c) * 4 + (r % 8) // 2, r % 2
+    k_at, k_high = ((t * 4 + r // 8) * nc + c) * 4 + (r % 8) // 2, r % 2
     v_at, v_high = 256 * nc + (((t // 4) * 16 + r % 16) * nc + c) * 4 + t % 4, r // 16
     ks_at, vs_at = 512 * nc + t * nc + c, 528 * nc + t * nc + c
     value = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64, device=DEV)
