@@ -3,4 +3,4 @@
 Importing the package loads nothing native; ``heterogeneous_adapters_amd.lora``
 loads ``liblora.so`` on first use and raises if it is missing.
 """
-__all__ = ["lora", "traffic"]
+__all__ = ["kv", "lora", "traffic"]
