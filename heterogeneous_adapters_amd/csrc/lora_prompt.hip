@@ -6,7 +6,7 @@
 //
 // bf16: a work-group of kWaves waves takes 32 rows per wave of one query
 // head and walks the prompt's keys in tiles of 64, copied straight into LDS
-// (global_load_lds, 16 bytes a lane) while the tile before is multiplied.
+// (buffer loads to LDS, 16 bytes a lane) while the tile before is multiplied.
 // v_mfma_f32_32x32x16_bf16 on both products: S^T = K Q^T leaves row lane%32
 // with tokens 8(i/4) + 4h + i%4 (h = lane/32) in each lane, which is the B
 // operand of O^T = V^T P^T once V^T is read in that token order
@@ -32,15 +32,14 @@ constexpr float kNone = -1e30f;  // running maximum before any key
 // 2^8 in p, without loss: p is scaled the same in the products and the sum).
 constexpr float kSlack = 8.0f;
 
-constexpr int kWaves = 4;
 constexpr int kRowsPerWave = 32;
-constexpr int kRows = kWaves * kRowsPerWave;
-constexpr int kKeys = 64;
+constexpr int kKeys = 64;  // keys per tile
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef const __attribute__((address_space(1))) void global_void;
+typedef const __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 
 // The prompt and tile of flat tile index w.  Prompt i's tiles start at
 // indptr[i] / rows + i, which leaves room for ceil(len / rows) of them; every
@@ -76,19 +75,33 @@ __device__ __forceinline__ int swz_v(int token, int piece) {
   return D % 64 == 0 ? piece ^ ((token & 3) << 1) : piece ^ (token & 2);
 }
 
-__device__ __forceinline__ bool bf_nonfinite(uint32_t w) {
-  return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no buffer descriptors
+// Buffer descriptor of the rest of a head's rows: loads behind the prompt's
+// last row return zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, (int)min(max(bytes, (int64_t)0), (int64_t)0xfffffff0ll),
+                                           0x00020000);
 }
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves) void prompt_kernel(const PromptArgs A) {
-  constexpr int kPieces = D / 8;       // 16-byte pieces per row
+#endif
+
+// s_waitcnt vmcnt(N) with the other counters left alone.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kRows = W * kRowsPerWave;
+  constexpr int kPieces = D / 8;  // 16-byte pieces per row
   constexpr int kTileBytes = kKeys * D * 2;
-  constexpr int kLoads = kTileBytes / (64 * kWaves * 16);  // per wave and tensor
-  static_assert(kTileBytes % (64 * kWaves * 16) == 0, "whole loads");
-  constexpr int kKSteps = D / 16, kDimTiles = D / 32;
-  __shared__ __attribute__((aligned(128))) uint8_t s_k[2][kTileBytes];
-  __shared__ __attribute__((aligned(128))) uint8_t s_v[2][kTileBytes];
+  constexpr int kLoads = kTileBytes / 1024;  // 1 KB loads per tensor, dealt to the waves
+  constexpr int kSteps = D / 16, kDims = D / 32;
+  // one array per buffer and tensor, so that the compiler sees which copy a
+  // read depends on
+  __shared__ __attribute__((aligned(128))) uint8_t s_k0[kTileBytes], s_v0[kTileBytes], s_k1[kTileBytes], s_v1[kTileBytes];
   __shared__ int s_found;
 
   const int hq_n = A.q.heads;
@@ -102,57 +115,73 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_kernel(const PromptArgs A)
   const int row_last = min(row_first + kRowsPerWave, sp.len) - 1;  // below row_first: no rows in this wave
   const int n_tiles = (min((sp.tile + 1) * kRows, sp.len) + kKeys - 1) / kKeys;
 
-  bf16x8 qf[kKSteps];
+  bf16x8 qf[kSteps];
   {
     const uint16_t* q = static_cast<const uint16_t*>(A.q.p) + (int64_t)(sp.begin + min(row, sp.len - 1)) * A.q.ts + hq * A.q.hs;
 #pragma unroll
-    for (int s = 0; s < kKSteps; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(q + 16 * s + 8 * h);
+    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(q + 16 * s + 8 * h);
   }
 
   const uint16_t* kbase = static_cast<const uint16_t*>(A.k.p) + (int64_t)sp.begin * A.k.ts + hk * A.k.hs;
   const uint16_t* vbase = static_cast<const uint16_t*>(A.v.p) + (int64_t)sp.begin * A.v.ts + hk * A.v.hs;
-  // Tokens behind the prompt's last read the last one's row; they are masked.
-  auto stage = [&](int tile, int buf) {
+  const int64_t kbytes = 2 * ((sp.len - 1) * A.k.ts + D), vbytes = 2 * ((sp.len - 1) * A.v.ts + D);
+  // Loads 0..kLoads-1 of a tile fetch K, the others V; wave w takes loads w,
+  // w + W, ..  The 16-byte place p of a tile holds piece swz(p) of its row.
+  constexpr int kMine = (2 * kLoads + W - 1) / W;
+  int off[kMine];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int at = (wave * kLoads + i) * 64 + lane;  // 16-byte place in the tile
-      const int token = at / kPieces, piece = at - token * kPieces;
-      const int64_t t = min(tile * kKeys + token, sp.len - 1);
-      __builtin_amdgcn_global_load_lds((global_void*)(kbase + t * A.k.ts + swz_k<D>(token, piece) * 8),
-                                       (lds_void*)(s_k[buf] + (wave * kLoads + i) * 1024), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((global_void*)(vbase + t * A.v.ts + swz_v<D>(token, piece) * 8),
-                                       (lds_void*)(s_v[buf] + (wave * kLoads + i) * 1024), 16, 0, 0);
+  for (int i = 0; i < kMine; ++i) {
+    const int load = wave + i * W, at = (load % kLoads) * 64 + lane;
+    const int token = at / kPieces, piece = at - token * kPieces;
+    off[i] = load < kLoads ? (int)(token * A.k.ts + swz_k<D>(token, piece) * 8) * 2
+                           : (int)(token * A.v.ts + swz_v<D>(token, piece) * 8) * 2;
+  }
+  auto stage = [&](int tile, uint8_t* sk, uint8_t* sv) {
+    const int64_t ko = (int64_t)tile * kKeys * A.k.ts, vo = (int64_t)tile * kKeys * A.v.ts;
+    const __amdgpu_buffer_rsrc_t kr = rows_rsrc(kbase + ko, kbytes - 2 * ko), vr = rows_rsrc(vbase + vo, vbytes - 2 * vo);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int load = wave + i * W;
+      if (load < kLoads)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(kr, (lds_void*)(sk + load * 1024), 16, off[i], 0, 0, 0);
+      else if (load < 2 * kLoads)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_void*)(sv + (load - kLoads) * 1024), 16, off[i], 0, 0, 0);
     }
   };
 
-  f16v o[kDimTiles];
+  // LDS places of this lane's K pieces (row n of a tile's 32, piece 2c + h)
+  // and V pieces (row 4h + i/4, dims 16 sub + 4 (i%4) of 32); the swizzle
+  // leaves kKVar and kVVar of them, the rest are constants away
+  constexpr int kKVar = D % 64 == 0 ? 4 : 2, kVVar = D % 64 == 0 ? 2 : 1;
+  int k_at[kKVar], v_at[kVVar];
 #pragma unroll
-  for (int d = 0; d < kDimTiles; ++d)
+  for (int c = 0; c < kKVar; ++c) k_at[c] = n * (2 * D) + swz_k<D>(n, 2 * c + h) * 16;
+  const int i16 = lane & 15, sub = (lane >> 4) & 1, v_row = 4 * h + (i16 >> 2);
+#pragma unroll
+  for (int d = 0; d < kVVar; ++d)
+    v_at[d] = v_row * (2 * D) + swz_v<D>(v_row, 4 * d + 2 * sub + ((i16 & 3) >> 1)) * 16 + (i16 & 1) * 8;
+
+  f16v o[kDims];
+#pragma unroll
+  for (int d = 0; d < kDims; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = kNone, l = 0.0f;
 
-  stage(0, 0);
-  for (int it = 0; it < n_tiles; ++it) {
-    const int buf = it & 1, key0 = it * kKeys;
-    __syncthreads();  // this tile has arrived, and the other buffer is free
-    if (it + 1 < n_tiles) stage(it + 1, buf ^ 1);
-    if (key0 > row_last) continue;
-
+  auto compute = [&](int key0, const uint8_t* sk, const uint8_t* sv) {
     f16v s[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
-      const int token = 32 * u + n;
 #pragma unroll
-      for (int c = 0; c < kKSteps; ++c) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(s_k[buf] + token * (2 * D) + swz_k<D>(token, 2 * c + h) * 16);
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) {
+        const bf16x8 a = *(lds_bf16x8*)(sk + k_at[c % kKVar] + u * 32 * (2 * D) + (c / kKVar) * (kKVar * 32));
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[c], s[u], 0, 0, 0);
       }
-    }
-    const bool masked = key0 + kKeys - 1 > row_first;
-    if (masked) {
+    if (key0 + kKeys - 1 > row_first) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -169,7 +198,7 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_kernel(const PromptArgs A)
       m = mn;
       l *= alpha;
 #pragma unroll
-      for (int d = 0; d < kDimTiles; ++d) o[d] *= alpha;
+      for (int d = 0; d < kDims; ++d) o[d] *= alpha;
     }
     bf16x8 pf[4];
 #pragma unroll
@@ -178,26 +207,36 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_kernel(const PromptArgs A)
       l += p;
       pf[i >> 3][i & 7] = (__bf16)p;
     }
-
-    // O^T += V^T P^T: lane i of each sixteen names token i/4, dims 4(i%4)..
-    const int i16 = lane & 15, sub = (lane >> 4) & 1;
+    // O^T += V^T P^T
 #pragma unroll
-    for (int d = 0; d < kDimTiles; ++d) {
-      const int dim = 32 * d + 16 * sub + 4 * (i16 & 3);
+    for (int c = 0; c < 4; ++c) {  // 16 tokens each
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // 16 tokens each
+      for (int d = 0; d < kDims; ++d) {
         s16x4 part[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int token = 16 * c + 8 * e + 4 * h + (i16 >> 2);
+        for (int e = 0; e < 2; ++e)
           part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4*)(s_v[buf] + token * (2 * D) + swz_v<D>(token, dim >> 3) * 16 + (dim & 4) * 2));
-        }
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
+              (lds_s16x4*)(sv + v_at[d % kVVar] + (16 * c + 8 * e) * (2 * D) + (d / kVVar) * (kVVar * 64)));
         const s16x8 a = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), pf[c], o[d], 0, 0, 0);
       }
     }
+  };
+
+  // Two tiles per turn, one per buffer.  Every wave waits for its own copies
+  // before the barrier that lets the others read them, whether it computes
+  // on the tile or not; past the barrier the other buffer is free.
+  stage(0, s_k0, s_v0);
+  for (int it = 0; it < n_tiles; it += 2) {
+    wait_vm<0>();
+    __syncthreads();
+    if (it + 1 < n_tiles) stage(it + 1, s_k1, s_v1);
+    if (it * kKeys <= row_last) compute(it * kKeys, s_k0, s_v0);
+    if (it + 1 >= n_tiles) break;
+    wait_vm<0>();
+    __syncthreads();
+    if (it + 2 < n_tiles) stage(it + 2, s_k0, s_v0);
+    if ((it + 1) * kKeys <= row_last) compute((it + 1) * kKeys, s_k1, s_v1);
   }
 
   l += __shfl_xor(l, 32);
@@ -205,7 +244,7 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_kernel(const PromptArgs A)
     const float inv = 1.0f / l;
     uint16_t* out = static_cast<uint16_t*>(A.o.p) + (int64_t)(sp.begin + row) * A.o.ts + hq * A.o.hs;
 #pragma unroll
-    for (int d = 0; d < kDimTiles; ++d)
+    for (int d = 0; d < kDims; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         uint2 w;
@@ -214,6 +253,7 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_kernel(const PromptArgs A)
         *reinterpret_cast<uint2*>(out + 32 * d + 2 * i + 4 * h) = w;
       }
   }
+#endif
 }
 
 // ------------------------------------------------------------------- fp32
@@ -292,8 +332,9 @@ __global__ __launch_bounds__(256) void prompt_f32_kernel(const PromptArgs A) {
 template <int D>
 hipError_t launch_d(const PromptArgs& A, int dtype, hipStream_t s) {
   if (dtype == LORA_DTYPE_BF16) {
-    const int64_t blocks = ((int64_t)A.T / kRows + A.B) * A.q.heads;
-    prompt_kernel<D><<<(unsigned)blocks, 64 * kWaves, 0, s>>>(A);
+    constexpr int W = 4;
+    const int64_t blocks = ((int64_t)A.T / (W * kRowsPerWave) + A.B) * A.q.heads;
+    prompt_kernel<D, W><<<(unsigned)blocks, 64 * W, 0, s>>>(A);
   } else {
     const int64_t blocks = ((int64_t)A.T / kRows32 + A.B) * A.q.heads;
     prompt_f32_kernel<D><<<(unsigned)blocks, 256, 0, s>>>(A);
