@@ -42,37 +42,51 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef const __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 
 // The prompt and tile of flat tile index w.  Prompt i's tiles start at
-// indptr[i] / rows + i, which leaves room for ceil(len / rows) of them; every
-// thread tests its share of the prompts.  Longest tiles come first.
+// indptr[i] / rows + i, which leaves room for ceil(len / rows) of them.  Each
+// wave searches by itself, 64 probes a step, and has the prompt's ends from
+// the last step's lanes: one trip to memory for up to 64 prompts and no
+// barrier.  Longest tiles come first.
 struct Span {
   int begin, len, tile;  // tile < 0: none
 };
 __device__ __forceinline__ int cut(int x, int T) { return min(max(x, 0), T); }
-__device__ __forceinline__ Span find_span(const PromptArgs& A, int w, int rows, int* found) {
-  if (threadIdx.x == 0) *found = -1;
-  __syncthreads();
-  for (int i = threadIdx.x; i < A.B; i += blockDim.x) {
-    const int a = cut(A.indptr[i], A.T), b = cut(A.indptr[i + 1], A.T);
-    const int local = w - (a / rows + i);
-    if (local >= 0 && (int64_t)local * rows < b - a) *found = i;
+__device__ __forceinline__ Span find_span(const PromptArgs& A, int w, int rows) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = A.B;  // the prompt is in [lo, hi)
+  while (true) {
+    const int step = (hi - lo + 63) / 64, p = lo + lane * step;
+    int a = 0, b = 0;
+    bool at_or_before = false;
+    if (p < hi) {
+      a = cut(A.indptr[p], A.T);
+      b = cut(A.indptr[p + 1], A.T);
+      at_or_before = a / rows + p <= w;
+    }
+    const int n = __popcll(__ballot(at_or_before));
+    if (n == 0) return Span{0, 0, -1};
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) {
+      const int begin = __builtin_amdgcn_readlane(a, n - 1), end = __builtin_amdgcn_readlane(b, n - 1);
+      const int local = w - (begin / rows + lo), tiles = (max(end - begin, 0) + rows - 1) / rows;
+      return Span{begin, end - begin, local >= 0 && local < tiles ? tiles - 1 - local : -1};
+    }
   }
-  __syncthreads();
-  const int i = uniform(*found);
-  if (i < 0) return Span{0, 0, -1};
-  const int a = uniform(cut(A.indptr[i], A.T)), b = uniform(cut(A.indptr[i + 1], A.T));
-  const int local = w - (a / rows + i);
-  return Span{a, b - a, (b - a + rows - 1) / rows - 1 - local};
 }
 
-// Swizzle of 16-byte pieces within a row of D elements: rows of a multiple of
-// 128 bytes start in the same bank, others alternate between two halves.
+// Swizzles of 16-byte pieces within a row of D elements, for 64 banks of 4
+// bytes: a K read takes one piece of 16 rows at a time, a V read 4 pieces
+// (64 bytes) of 4 rows.  Rows of a multiple of 256 bytes all start in the
+// same bank, of 128 bytes alternate between two places, others walk through
+// four; the swizzle spreads what the rows' starts do not.  (Spread over 128
+// bytes only, half the LDS cycles were conflicts.)
 template <int D>
 __device__ __forceinline__ int swz_k(int token, int piece) {
-  return D % 64 == 0 ? piece ^ (token & 7) : piece ^ ((token >> 1) & 3);
+  return D % 128 == 0 ? piece ^ (token & 15) : D % 64 == 0 ? piece ^ ((token >> 1) & 7) : piece ^ ((token >> 2) & 3);
 }
 template <int D>
 __device__ __forceinline__ int swz_v(int token, int piece) {
-  return D % 64 == 0 ? piece ^ ((token & 3) << 1) : piece ^ (token & 2);
+  return D % 128 == 0 ? piece ^ ((token & 3) << 2) : D % 64 == 0 ? piece ^ ((token & 2) << 1) : piece;
 }
 
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no buffer descriptors
@@ -102,11 +116,10 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
   // one array per buffer and tensor, so that the compiler sees which copy a
   // read depends on
   __shared__ __attribute__((aligned(128))) uint8_t s_k0[kTileBytes], s_v0[kTileBytes], s_k1[kTileBytes], s_v1[kTileBytes];
-  __shared__ int s_found;
 
   const int hq_n = A.q.heads;
   const int flat = blockIdx.x / hq_n, hq = blockIdx.x - flat * hq_n, hk = hq / A.G;
-  const Span sp = find_span(A, flat, kRows, &s_found);
+  const Span sp = find_span(A, flat, kRows);
   if (sp.tile < 0) return;
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
@@ -152,7 +165,7 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
   // LDS places of this lane's K pieces (row n of a tile's 32, piece 2c + h)
   // and V pieces (row 4h + i/4, dims 16 sub + 4 (i%4) of 32); the swizzle
   // leaves kKVar and kVVar of them, the rest are constants away
-  constexpr int kKVar = D % 64 == 0 ? 4 : 2, kVVar = D % 64 == 0 ? 2 : 1;
+  constexpr int kKVar = D % 128 == 0 ? 8 : D % 64 == 0 ? 4 : 2, kVVar = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1;
   int k_at[kKVar], v_at[kVVar];
 #pragma unroll
   for (int c = 0; c < kKVar; ++c) k_at[c] = n * (2 * D) + swz_k<D>(n, 2 * c + h) * 16;
@@ -181,6 +194,23 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
         const bf16x8 a = *(lds_bf16x8*)(sk + k_at[c % kKVar] + u * 32 * (2 * D) + (c / kKVar) * (kKVar * 32));
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[c], s[u], 0, 0, 0);
       }
+#pragma unroll
+    for (int i = 0; i < kSteps * 2 - 6; ++i) {
+      if (i == 0) __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
+    s16x8 vf[kDims];
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      s16x4 part[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(sv + v_at[d % kVVar] + 8 * e * (2 * D) + (d / kVVar) * (kVVar * 64)));
+      vf[d] = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
     if (key0 + kKeys - 1 > row_first) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -217,7 +247,7 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
         for (int e = 0; e < 2; ++e)
           part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (lds_s16x4*)(sv + v_at[d % kVVar] + (16 * c + 8 * e) * (2 * D) + (d / kVVar) * (kVVar * 64)));
-        const s16x8 a = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const s16x8 a = c == 0 ? vf[d] : __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), pf[c], o[d], 0, 0, 0);
       }
     }
@@ -262,10 +292,9 @@ constexpr int kRows32 = 64;  // rows per work-group, 16 per wave
 template <int D>
 __global__ __launch_bounds__(256) void prompt_f32_kernel(const PromptArgs A) {
   constexpr int kVecs = D / 16;
-  __shared__ int s_found;
   const int hq_n = A.q.heads;
   const int flat = blockIdx.x / hq_n, hq = blockIdx.x - flat * hq_n, hk = hq / A.G;
-  const Span sp = find_span(A, flat, kRows32, &s_found);
+  const Span sp = find_span(A, flat, kRows32);
   if (sp.tile < 0) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
   const int row_first = sp.tile * kRows32 + wave * 16, row = row_first + n;
