@@ -14,7 +14,7 @@ using namespace lora::kv;
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxBlocks = (int64_t)1 << 24;  // work-groups of 256 threads: a launch has under 2^32 threads
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // work-groups of 512 threads: a launch has under 2^32 threads
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -90,7 +90,7 @@ BatchSizes batch_sizes(int32_t max_tokens, int32_t max_seqs, int32_t hq, int32_t
   z.kv_len = align_up(4 * (size_t)max_seqs);
   z.row = align_up(4 * (size_t)std::max(max_tokens, 1));
   z.counts = align_up(4 * kNumCounts);
-  z.items = align_up(16 * (size_t)item_cap(max_tokens, max_seqs, hkv, hq / hkv));
+  z.items = align_up(2 * 16 * (size_t)item_cap(max_tokens, max_seqs, hkv, hq / hkv));
   z.arrive = align_up(4 * (size_t)part_cap(hkv) * hkv);
   z.total = z.q_indptr + z.kv_len + 3 * z.row + z.counts + z.items + z.arrive;
   return z;
@@ -378,7 +378,7 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
   A.scale_log2e = scale * 1.4426950408889634f;
   A.part = static_cast<float*>(ws);
   const int64_t blocks = item_cap(T, B, batch->num_kv_heads, A.G) * batch->num_kv_heads;
-  return hip(launch_attend(A, dtype, (int)blocks, static_cast<hipStream_t>(stream)));
+  return hip(launch_attend(A, dtype, (int)blocks, wide_step(T, B), static_cast<hipStream_t>(stream)));
 }
 
 lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, const lora_heads_t* v,

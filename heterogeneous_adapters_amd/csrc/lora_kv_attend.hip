@@ -5,9 +5,10 @@
 // request are split into chunks (lora_kv_build's plan); chunks of one row are
 // joined by o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 //
-// A work item is (16 rows = new tokens x heads that share a kv head, one
-// chunk, one kv head), walked by a work-group of 4 waves that take every
-// fourth step of 32 tokens and join their results in LDS.  Per step a wave
+// A work item is (16 or 32 rows = new tokens x heads that share a kv head, one
+// chunk, one kv head), walked by a work-group whose waves take turns at steps
+// of 32 tokens and join their results in LDS; the work-group that finishes a
+// row's last chunk joins the chunks.  Per step a wave
 // reads the 17/16 byte per value pair once, converts the codes to bf16 with
 // v_cvt_scalef32_pk_bf16_fp4 (exact), and multiplies on
 // v_mfma_f32_16x16x32_bf16: S^T = K Q^T, whose result layout (row = lane%16,
@@ -22,11 +23,21 @@ namespace kv {
 
 namespace {
 
-constexpr int kThreads = 64 * kAttendWaves;
 constexpr float kNone = -1e30f;  // running maximum before any visible key
 // Rows keep their maximum until a score passes it by this much (a factor of
 // 2^8 in p, without loss: p is scaled the same in the products and the sum).
 constexpr float kSlack = 8.0f;
+
+// Partial results cross XCDs within the launch: agent-scope accesses (write
+// through, and past the reader's own L2), 8 bytes each, no cache maintenance.
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  const uint64_t u = (uint64_t)__float_as_uint(a) | (uint64_t)__float_as_uint(b) << 32;
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get2(const float* p) {
+  const uint64_t u = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)));
+}
 
 template <int NC>
 struct Step {  // one wave's 32 tokens: two units' records
@@ -77,61 +88,80 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&f)[NS]) {
   }
 }
 
-template <class E, int NC>
-__global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
+// Whether the batch's plan was built for this call.
+__device__ __forceinline__ bool plan_ok(const AttendArgs& A) {
+  const int32_t* c = A.counts;
+  return c[kCountCheck] == check_word(c[kCountB], c[kCountT], c[kCountItems], c[kCountWide], c[kCountParts]) &&
+         c[kCountB] == A.B && c[kCountT] == A.T && c[kCountItems] <= A.item_cap && c[kCountWide] <= A.item_cap;
+}
+
+// Reciprocal of a row's sum: zero for a row that saw no key, NaN kept.
+__device__ __forceinline__ float inverse(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l); }
+
+// RT: tiles of 16 rows per work item (1, or 2 for requests of many rows).
+// W: waves per work-group.
+template <class E, int NC, int RT, int W>
+__global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T) == 2 ? 4 : 1) void attend_kernel(const AttendArgs A) {
+  constexpr int kThreads = 64 * W;
   constexpr int NS = sizeof(typename E::T) == 2 ? 1 : 3;
-  constexpr int D = 32 * NC, LD = D + 4;
+  constexpr int D = 32 * NC, LD = D + 4, kVecs = D / 4;
   typedef typename E::T T;
-  __shared__ float s_o[kAttendWaves][kUnit][LD];
-  __shared__ float s_m[kAttendWaves][kUnit], s_l[kAttendWaves][kUnit];
+  __shared__ float s_o[W][kUnit][LD];
+  __shared__ float s_m[W][kUnit], s_l[W][kUnit];
+  __shared__ int s_last;
 
   const int hkv = A.cache.heads;
   const int item = blockIdx.x / hkv, kvh = blockIdx.x - item * hkv;
-  const int n_items = A.counts[kCountItems], n_parts = A.counts[kCountParts], chunk = A.counts[kCountChunk];
-  if (A.counts[kCountCheck] != check_word(A.counts[kCountB], A.counts[kCountT], n_items, n_parts) ||
-      A.counts[kCountB] != A.B || A.counts[kCountT] != A.T || n_items > A.item_cap) {
+  if (!plan_ok(A)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
     return;
   }
-  if (item >= n_items) return;
-  const int4 desc = A.items[item];
+  if (item >= A.counts[RT == 1 ? kCountItems : kCountWide]) return;
+  const int chunk = A.counts[kCountChunk];
+  const int4 desc = A.items[RT == 1 ? item : A.item_cap + item];
   const int seq = uniform(desc.x), tile = uniform(desc.y), ci = uniform(desc.z), part = uniform(desc.w);
   const int qs = uniform(A.q_indptr[seq]), qe = uniform(A.q_indptr[seq + 1]), kv = uniform(A.kv_len[seq]);
-  const int G = A.G, nrows = (qe - qs) * G, row0 = tile * kUnit;
+  const int G = A.G, nrows = (qe - qs) * G, row0 = tile * (kUnit * RT);
   const int pos0 = uniform(A.positions[qs]);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-  const int row = row0 + n, rowc = min(row, nrows - 1);
-  const int jq = rowc / G, hq = kvh * G + rowc - jq * G;
-  const int limit = min(pos0 + jq + 1, kv);  // this lane's row sees tokens below this
   const int limit0 = uniform(min(pos0 + row0 / G + 1, kv));
   const int begin = ci * chunk;
-  const int end = min(begin + chunk, uniform(min(pos0 + min(row0 + kUnit - 1, nrows - 1) / G + 1, kv)));
+  const int end = min(begin + chunk, uniform(min(pos0 + min(row0 + kUnit * RT - 1, nrows - 1) / G + 1, kv)));
 
-  bf16x8 qf[NC][NS];
-  {
-    const T* q = static_cast<const T*>(A.q.p) + (int64_t)(qs + jq) * A.q.ts + hq * A.q.hs;
+  int limit[RT];  // this lane's rows see tokens below these
+  bf16x8 qf[RT][NC][NS];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = min(row0 + r * kUnit + n, nrows - 1), jq = row / G;
+    limit[r] = min(pos0 + jq + 1, kv);
+    const T* q = static_cast<const T*>(A.q.p) + (int64_t)(qs + jq) * A.q.ts + (kvh * G + row - jq * G) * A.q.hs;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float x[8];
       load_n<8>(q + 32 * c + 8 * g, x);
-      split8<NS>(x, qf[c]);
+      split8<NS>(x, qf[r][c]);
     }
   }
 
-  f4 o[NC][2];
+  f4 o[RT][NC][2];
+  float m[RT], l[RT];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) o[c][0] = o[c][1] = f4{0, 0, 0, 0};
-  float m = kNone, l = 0.0f;
+  for (int r = 0; r < RT; ++r) {
+    m[r] = kNone;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) o[r][c][0] = o[r][c][1] = f4{0, 0, 0, 0};
+  }
 
   const int32_t* trow = A.table + (int64_t)seq * A.tstride;
   const uint8_t* head = A.cache.base + ((int64_t)kvh << A.cache.bt_log2 >> 4) * (544 * NC);
   const int unit_mask = (1 << (A.cache.bt_log2 - 4)) - 1;
-  const int first = begin / kTile + wave, last = (end + kTile - 1) / kTile;  // steps first, first+4, .. < last
+  const int first = begin / kTile + wave, last = (end + kTile - 1) / kTile;  // steps first, first+W, .. < last
   bool bad_block = false;
 
   // Block ids of 32 steps, two units each, one per lane; -1 outside the cache.
   auto fetch_ids = [&](int step) {
-    const int token = (step + kAttendWaves * (lane >> 1)) * kTile + kUnit * (lane & 1);
+    const int token = (step + W * (lane >> 1)) * kTile + kUnit * (lane & 1);
     int id = 0;
     if (token < end) {
       id = trow[token >> A.cache.bt_log2];
@@ -154,8 +184,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
     int id0 = __builtin_amdgcn_readlane(ids, 0), id1 = __builtin_amdgcn_readlane(ids, 1);
     load_step(cur, id0, id1, first);
     int k = 0;  // place of the current step among the fetched ids
-    for (int step = first; step < last; step += kAttendWaves) {
-      const int next = step + kAttendWaves;
+    for (int step = first; step < last; step += W) {
+      const int next = step + W;
       int nid0 = 0, nid1 = 0;
       if (++k == 32) {
         k = 0;
@@ -168,17 +198,20 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
       }
 
       // S^T = K Q^T
-      f4 s[2];
+      f4 s[RT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        s[u] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r][u] = f4{0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const float sc = __uint_as_float((uint32_t)cur.ks[u][c] << 23);
           const uint32_t w = cur.k[u][c];
           const bf16x8 a = frag(fp4_pair(w, sc, 0), fp4_pair(w, sc, 1), fp4_pair(w, sc, 2), fp4_pair(w, sc, 3));
 #pragma unroll
-          for (int t = 0; t < NS; ++t) s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[c][t], s[u], 0, 0, 0);
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NS; ++t) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[r][c][t], s[r][u], 0, 0, 0);
         }
       }
       const int tok = step * kTile;
@@ -189,7 +222,9 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
           uint32_t keep = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (id < 0 || t0 + i >= limit) s[u][i] = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              if (id < 0 || t0 + i >= limit[r]) s[r][u][i] = -INFINITY;
             if (id >= 0 && t0 + i < end) keep |= 0xffu << (8 * i);
           }
           // bytes behind the last token may hold anything, a scale of NaN
@@ -204,25 +239,28 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
         }
       }
 
-      float most = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                         fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * A.scale_log2e;
-      if (__any(most > m + kSlack)) {
-        most = fmaxf(most, __shfl_xor(most, 16));
-        most = fmaxf(most, __shfl_xor(most, 32));
-        const float mn = fmaxf(m, most), alpha = exp2_hw(m - mn);
-        m = mn;
-        l *= alpha;
+      bf16x8 pf[RT][NS];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[c][0] *= alpha, o[c][1] *= alpha;
-      }
-      float p[8];
+      for (int r = 0; r < RT; ++r) {
+        float most = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                           fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * A.scale_log2e;
+        if (__any(most > m[r] + kSlack)) {
+          most = fmaxf(most, __shfl_xor(most, 16));
+          most = fmaxf(most, __shfl_xor(most, 32));
+          const float mn = fmaxf(m[r], most), alpha = exp2_hw(m[r] - mn);
+          m[r] = mn;
+          l[r] *= alpha;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = exp2_hw(fmaf(s[i >> 2][i & 3], A.scale_log2e, -m));
-        l += p[i];
+          for (int c = 0; c < NC; ++c) o[r][c][0] *= alpha, o[r][c][1] *= alpha;
+        }
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = exp2_hw(fmaf(s[r][i >> 2][i & 3], A.scale_log2e, -m[r]));
+          l[r] += p[i];
+        }
+        split8<NS>(p, pf[r]);
       }
-      bf16x8 pf[NS];
-      split8<NS>(p, pf);
 
       // O^T += V^T P^T
 #pragma unroll
@@ -243,10 +281,12 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
         }
         const bf16x8 alo = frag(lo[0], lo[1], lo[2], lo[3]), ahi = frag(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
-        for (int t = 0; t < NS; ++t) {
-          o[c][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(alo, pf[t], o[c][0], 0, 0, 0);
-          o[c][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ahi, pf[t], o[c][1], 0, 0, 0);
-        }
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int t = 0; t < NS; ++t) {
+            o[r][c][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(alo, pf[r][t], o[r][c][0], 0, 0, 0);
+            o[r][c][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ahi, pf[r][t], o[r][c][1], 0, 0, 0);
+          }
       }
       cur = nxt;
       id0 = nid0;
@@ -255,112 +295,166 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs A) {
   }
   if (__any(bad_block) && lane == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BLOCK_RANGE);
 
-  // join the four waves
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  // Output rows of tile r; a row's four dims from d.
+  auto store = [&](int r, int i, int d, f4 acc, float inv) {
+    const int row = row0 + r * kUnit + i, jr = row / G;
+    T* out = static_cast<T*>(A.o.p) + (int64_t)(qs + jr) * A.o.ts + (kvh * G + row - jr * G) * A.o.hs + d;
+    if constexpr (sizeof(T) == 2) {
+      uint2 w;
+      w.x = pack_bf2(acc[0] * inv, acc[1] * inv);
+      w.y = pack_bf2(acc[2] * inv, acc[3] * inv);
+      *reinterpret_cast<uint2*>(out) = w;
+    } else {
+      *reinterpret_cast<f4*>(out) = acc * inv;
+    }
+  };
+  // A part (16 rows of one chunk): rows of D sums, then (m, l) pairs.
+  constexpr int kPart = kUnit * (D + 2);
+  auto part_at = [&](int c, int r) { return A.part + ((int64_t)(part + c * RT + r) * hkv + kvh) * kPart; };
+
+  // join the waves
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    *reinterpret_cast<f4*>(&s_o[wave][n][32 * c + 4 * g]) = o[c][0];
-    *reinterpret_cast<f4*>(&s_o[wave][n][32 * c + 16 + 4 * g]) = o[c][1];
+  for (int r = 0; r < RT; ++r) {
+    if (r) __syncthreads();
+    float lr = l[r];
+    lr += __shfl_xor(lr, 16);
+    lr += __shfl_xor(lr, 32);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      *reinterpret_cast<f4*>(&s_o[wave][n][32 * c + 4 * g]) = o[r][c][0];
+      *reinterpret_cast<f4*>(&s_o[wave][n][32 * c + 16 + 4 * g]) = o[r][c][1];
+    }
+    if (g == 0) {
+      s_m[wave][n] = m[r];
+      s_l[wave][n] = lr;
+    }
+    __syncthreads();
+    const int live = min(nrows - row0 - r * kUnit, kUnit);
+    for (int i = threadIdx.x; i < live * kVecs; i += kThreads) {
+      const int row = i / kVecs, d = (i - row * kVecs) * 4;
+      float M = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][row]);
+      float L = 0.0f;
+      f4 acc{0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float a = exp2_hw(s_m[w][row] - M);
+        L += a * s_l[w][row];
+        acc += a * *reinterpret_cast<const f4*>(&s_o[w][row][d]);
+      }
+      if (part < 0) {
+        store(r, row, d, acc, inverse(L));
+      } else {
+        float* p = part_at(ci, r);
+        put2(p + row * D + d, acc[0], acc[1]);
+        put2(p + row * D + d + 2, acc[2], acc[3]);
+        if (d == 0) put2(p + kUnit * D + 2 * row, M, L);
+      }
+    }
   }
-  if (g == 0) {
-    s_m[wave][n] = m;
-    s_l[wave][n] = l;
+  if (part < 0) return;
+
+  // The work-group that finishes a tile's last chunk joins the chunks, in
+  // their order, whichever it is.  Its own wait makes a part's stores visible
+  // before its arrival is counted.
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  wait_vm<0>();
+  __syncthreads();
+  const int chunks = (kv + chunk - 1) / chunk;
+  if (threadIdx.x == 0) {
+    int32_t* count = A.arrive + (int64_t)part * hkv + kvh;
+    const int before = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = before == chunks - 1;
+    if (s_last) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next layer
   }
   __syncthreads();
-  constexpr int kVec = kUnit * D / 4;  // vectors of 4 dims of the tile
-  for (int i = threadIdx.x; i < kVec; i += kThreads) {
-    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-    if (row0 + r >= nrows) break;
-    float M = s_m[0][r];
+  if (!s_last) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+  float* s_join = &s_o[0][0][0];
 #pragma unroll
-    for (int w = 1; w < kAttendWaves; ++w) M = fmaxf(M, s_m[w][r]);
-    float L = 0.0f;
-    f4 acc{0, 0, 0, 0};
+  for (int r = 0; r < RT; ++r) {
+    const int live = min(nrows - row0 - r * kUnit, kUnit);
+    if (live <= 0) break;
+    const int tasks = live * kVecs;
+    const int groups = max(1, min(kThreads / tasks, chunks));  // threads per task, each every groups-th chunk
+    for (int t0 = 0; t0 < tasks; t0 += kThreads) {  // more than one turn only with one group
+      const int grp = threadIdx.x / tasks, task = t0 + threadIdx.x - (groups > 1 ? grp * tasks : 0);
+      const int row = task / kVecs, d = (task - row * kVecs) * 4;
+      const bool work = task < tasks && (groups == 1 || grp < groups);
+      float M = kNone, L = 0.0f;
+      f4 acc{0, 0, 0, 0};
+      if (work) {
+        for (int c = groups > 1 ? grp : 0; c < chunks; c += 4 * groups) {
+          float2 ml[4], lo[4], hi[4];
 #pragma unroll
-    for (int w = 0; w < kAttendWaves; ++w) {
-      const float a = exp2_hw(s_m[w][r] - M);
-      L += a * s_l[w][r];
-      acc += a * *reinterpret_cast<const f4*>(&s_o[w][r][d]);
-    }
-    if (part < 0) {
-      const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);  // no visible key: zeros; NaN stays
-      const int jr = (row0 + r) / G, h = kvh * G + row0 + r - jr * G;
-      T* out = static_cast<T*>(A.o.p) + (int64_t)(qs + jr) * A.o.ts + h * A.o.hs + d;
+          for (int e = 0; e < 4; ++e) {
+            const float* p = part_at(min(c + e * groups, chunks - 1), r);
+            ml[e] = get2(p + kUnit * D + 2 * row);
+            lo[e] = get2(p + row * D + d);
+            hi[e] = get2(p + row * D + d + 2);
+          }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) from_f(out + e, acc[e] * inv);
-    } else {
-      float* p = A.part + ((int64_t)(part + ci) * hkv + kvh) * (kUnit * (D + 2));
-      if (d == 0) p[r] = M, p[kUnit + r] = L;
-      *reinterpret_cast<f4*>(p + 2 * kUnit + r * D + d) = acc;
+          for (int e = 0; e < 4; ++e) {
+            if (c + e * groups >= chunks) break;
+            const float mn = fmaxf(M, ml[e].x), a = exp2_hw(M - mn), b = exp2_hw(ml[e].x - mn);
+            M = mn;
+            L = L * a + ml[e].y * b;
+            acc = acc * a + b * f4{lo[e].x, lo[e].y, hi[e].x, hi[e].y};
+          }
+        }
+      }
+      if (groups > 1) {
+        __syncthreads();
+        if (work) {
+          float* s = s_join + threadIdx.x * 6;
+          s[0] = M, s[1] = L;
+          s[2] = acc[0], s[3] = acc[1], s[4] = acc[2], s[5] = acc[3];
+        }
+        __syncthreads();
+        if (work && grp == 0) {
+          for (int e = 1; e < groups; ++e) {
+            const float* s = s_join + (threadIdx.x + e * tasks) * 6;
+            const float mn = fmaxf(M, s[0]), a = exp2_hw(M - mn), b = exp2_hw(s[0] - mn);
+            M = mn;
+            L = L * a + s[1] * b;
+            acc = acc * a + b * f4{s[2], s[3], s[4], s[5]};
+          }
+        }
+      }
+      if (work && grp == 0) store(r, row, d, acc, inverse(L));
+      if (groups > 1) break;
     }
   }
 }
 
-// Joins the chunks of a tile.
 template <class E, int NC>
-__global__ __launch_bounds__(kThreads) void join_kernel(const AttendArgs A) {
-  constexpr int D = 32 * NC;
-  typedef typename E::T T;
-  const int hkv = A.cache.heads;
-  const int item = blockIdx.x / hkv, kvh = blockIdx.x - item * hkv;
-  const int n_items = A.counts[kCountItems], n_parts = A.counts[kCountParts], chunk = A.counts[kCountChunk];
-  if (A.counts[kCountCheck] != check_word(A.counts[kCountB], A.counts[kCountT], n_items, n_parts) ||
-      A.counts[kCountB] != A.B || A.counts[kCountT] != A.T || item >= n_items || n_items > A.item_cap)
-    return;
-  const int4 desc = A.items[item];
-  if (desc.z != 0 || desc.w < 0) return;
-  const int seq = desc.x, row0 = desc.y * kUnit, G = A.G;
-  const int qs = A.q_indptr[seq], nrows = (A.q_indptr[seq + 1] - qs) * G;
-  const int chunks = (A.kv_len[seq] + chunk - 1) / chunk;
-  const float* p0 = A.part + ((int64_t)desc.w * hkv + kvh) * (kUnit * (D + 2));
-  const int64_t stride = (int64_t)hkv * (kUnit * (D + 2));
-  for (int i = threadIdx.x; i < kUnit * D / 4; i += kThreads) {
-    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-    if (row0 + r >= nrows) break;
-    float M = kNone;
-    for (int c = 0; c < chunks; ++c) M = fmaxf(M, p0[c * stride + r]);
-    float L = 0.0f;
-    f4 acc{0, 0, 0, 0};
-    for (int c = 0; c < chunks; ++c) {
-      const float* p = p0 + c * stride;
-      const float a = exp2_hw(p[r] - M);
-      L += a * p[kUnit + r];
-      acc += a * *reinterpret_cast<const f4*>(p + 2 * kUnit + r * D + d);
-    }
-    const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
-    const int jr = (row0 + r) / G, h = kvh * G + row0 + r - jr * G;
-    T* out = static_cast<T*>(A.o.p) + (int64_t)(qs + jr) * A.o.ts + h * A.o.hs + d;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) from_f(out + e, acc[e] * inv);
-  }
-}
-
-template <class E, int NC>
-hipError_t launch(const AttendArgs& A, int blocks, hipStream_t s) {
-  attend_kernel<E, NC><<<blocks, kThreads, 0, s>>>(A);
-  join_kernel<E, NC><<<blocks, kThreads, 0, s>>>(A);
+hipError_t launch(const AttendArgs& A, int blocks, bool wide, hipStream_t s) {
+  // 8 waves join through 64 KB of LDS at 128 dims; past that, 4
+  constexpr int W = NC <= 4 ? 8 : 4;
+  if (wide) attend_kernel<E, NC, 2, W><<<blocks, 64 * W, 0, s>>>(A);
+  attend_kernel<E, NC, 1, W><<<blocks, 64 * W, 0, s>>>(A);
   return hipGetLastError();
 }
 
 template <class E>
-hipError_t launch_nc(const AttendArgs& A, int blocks, hipStream_t s) {
+hipError_t launch_nc(const AttendArgs& A, int blocks, bool wide, hipStream_t s) {
   switch (A.cache.nc) {
-    case 1: return launch<E, 1>(A, blocks, s);
-    case 2: return launch<E, 2>(A, blocks, s);
-    case 3: return launch<E, 3>(A, blocks, s);
-    case 4: return launch<E, 4>(A, blocks, s);
-    case 5: return launch<E, 5>(A, blocks, s);
-    case 6: return launch<E, 6>(A, blocks, s);
-    case 7: return launch<E, 7>(A, blocks, s);
-    default: return launch<E, 8>(A, blocks, s);
+    case 1: return launch<E, 1>(A, blocks, wide, s);
+    case 2: return launch<E, 2>(A, blocks, wide, s);
+    case 3: return launch<E, 3>(A, blocks, wide, s);
+    case 4: return launch<E, 4>(A, blocks, wide, s);
+    case 5: return launch<E, 5>(A, blocks, wide, s);
+    case 6: return launch<E, 6>(A, blocks, wide, s);
+    case 7: return launch<E, 7>(A, blocks, wide, s);
+    default: return launch<E, 8>(A, blocks, wide, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, hipStream_t s) {
-  return dtype == LORA_DTYPE_BF16 ? launch_nc<Bf16>(A, blocks, s) : launch_nc<F32>(A, blocks, s);
+hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, bool wide, hipStream_t s) {
+  return dtype == LORA_DTYPE_BF16 ? launch_nc<Bf16>(A, blocks, wide, s) : launch_nc<F32>(A, blocks, wide, s);
 }
 
 }  // namespace kv

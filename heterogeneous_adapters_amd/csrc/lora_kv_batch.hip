@@ -78,6 +78,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   __shared__ int32_t s_row[kThreads];    // first token row
   __shared__ int32_t s_fresh[kThreads];  // first new block, counted over the step
   __shared__ int32_t s_item[kThreads];   // first work item
+  __shared__ int32_t s_wide[kThreads];   // first work item of 32 rows
   __shared__ int32_t s_ctx[kThreads], s_chunks[kThreads], s_part[kThreads];
   const int tid = threadIdx.x, wg = blockIdx.x, nwg = gridDim.x;
   const int bt = 1 << A.bt_log2;
@@ -95,8 +96,9 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   const int64_t rounded = max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)kMinChunk);
   const int chunk = (int)min(rounded, (int64_t)1 << 30);
 
+  const bool wide_ok = wide_step(A.T, A.B);
   int64_t rows0 = 0, fresh0 = 0;
-  int items0 = 0, parts0 = 0, flags = 0;
+  int items0 = 0, wide0 = 0, parts0 = 0, flags = 0;
   for (int base = 0; base < A.B; base += kThreads) {
     const int i = base + tid;
     const Request r = request(A, i, cap);
@@ -107,18 +109,22 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
     const int64_t fresh_first = fresh_end - (r.need - r.have);
     const int got = (int)max(min((int64_t)A.nfree - fresh_first, (int64_t)(r.need - r.have)), (int64_t)0);
     const int kv = (int)min(min((int64_t)r.ctx + (last - first), (int64_t)cap), (int64_t)(r.have + got) << A.bt_log2);
-    int tiles = (int)tiles_of(last - first, A.G);
-    const int chunks = (kv + chunk - 1) / chunk;
-    int items, parts;
-    const int n_items = i < A.B ? tiles * max(chunks, 1) : 0;
-    const int n_parts = chunks > 1 ? n_items : 0;
+    const bool wide = wide_ok && (int64_t)(last - first) * A.G > kUnit;
+    const int tiles = (int)(((int64_t)(last - first) * A.G + (wide ? 2 * kUnit - 1 : kUnit - 1)) / (wide ? 2 * kUnit : kUnit));
+    const int chunks = max((kv + chunk - 1) / chunk, 1);
+    int items, wides, parts;
+    const int n_all = i < A.B ? tiles * chunks : 0;
+    const int n_items = wide ? 0 : n_all, n_wide = wide ? n_all : 0;
+    const int n_parts = chunks > 1 ? n_items + 2 * n_wide : 0;
     const int item_end = items0 + block_scan<int32_t>(n_items, scratch_i, &items);
+    const int wide_end = wide0 + block_scan<int32_t>(n_wide, scratch_i, &wides);
     const int part_end = parts0 + block_scan<int32_t>(n_parts, scratch_i, &parts);
     s_row[tid] = first;
     s_fresh[tid] = (int)min(fresh_first, (int64_t)0x7fffffff);
     s_item[tid] = item_end - n_items;
+    s_wide[tid] = wide_end - n_wide;
     s_ctx[tid] = r.ctx;
-    s_chunks[tid] = max(chunks, 1);
+    s_chunks[tid] = chunks;
     s_part[tid] = chunks > 1 ? part_end - n_parts : -1;
     if (wg == 0 && i < A.B) {
       A.q_indptr[i] = first;
@@ -165,21 +171,27 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       for (int64_t f = fresh0 + tid; f < min(fresh1, (int64_t)A.nfree); f += kThreads)
         if ((unsigned)A.free_blocks[f] >= (unsigned)A.blocks) flags |= LORA_KV_FLAG_BLOCK_RANGE;
     }
-    for (int w = items0 + wg * kThreads + tid; w < min(items0 + items, A.item_cap); w += nwg * kThreads) {
-      const int k = bisect(s_item, n, w);
-      const int local = w - s_item[k], tile = local / s_chunks[k], c = local - tile * s_chunks[k];
+    // One item: its request, tile, chunk and the tile's first part (-1: alone).
+    auto fill = [&](const int32_t* start, int w, int units, int4* to) {
+      const int k = bisect(start, n, w);
+      const int local = w - start[k], tile = local / s_chunks[k], c = local - tile * s_chunks[k];
       int part = -1;
       if (s_part[k] >= 0) {
-        part = s_part[k] + tile * s_chunks[k];  // the tile's first part
-        if (part + s_chunks[k] > A.part_cap) part = -1;
+        part = s_part[k] + tile * s_chunks[k] * units;
+        if (part + s_chunks[k] * units > A.part_cap) part = -1;
         if (part >= 0)
           for (int h = 0; c == 0 && h < A.hkv; ++h) A.arrive[(int64_t)part * A.hkv + h] = 0;
       }
-      A.items[w] = make_int4(base + k, tile, c, part);
-    }
+      *to = make_int4(base + k, tile, c, part);
+    };
+    for (int w = items0 + wg * kThreads + tid; w < min(items0 + items, A.item_cap); w += nwg * kThreads)
+      fill(s_item, w, 1, A.items + w);
+    for (int w = wide0 + wg * kThreads + tid; w < min(wide0 + wides, A.item_cap); w += nwg * kThreads)
+      fill(s_wide, w, 2, A.items + A.item_cap + w);
     rows0 += rows;
     fresh0 += fresh;
     items0 += items;
+    wide0 += wides;
     parts0 += parts;
     __syncthreads();
   }
@@ -205,11 +217,12 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       if (tid == kCountNewBlocks) v = (int)min(fresh0, (int64_t)0x7fffffff);
       if (tid == kCountItems) v = items0;
       if (tid == kCountParts) v = parts0;
+      if (tid == kCountWide) v = wide0;
       if (tid == kCountChunk) v = chunk;
       if (tid == kCountFlags) v = all;
       if (tid == kCountB) v = A.B;
       if (tid == kCountT) v = A.T;
-      if (tid == kCountCheck) v = check_word(A.B, A.T, items0, parts0);
+      if (tid == kCountCheck) v = check_word(A.B, A.T, items0, wide0, parts0);
       A.counts[tid] = v;
     }
     if (tid == kThreads - 1) A.q_indptr[A.B] = used;

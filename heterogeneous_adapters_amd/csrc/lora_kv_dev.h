@@ -89,6 +89,12 @@ __device__ __forceinline__ void store_n(float* p, const float (&x)[N]) {
   }
 }
 
+// s_waitcnt vmcnt(N) with the other counters left alone.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
 // The scale of one cached group as the fp32 number whose exponent is scale
 // byte `k` of a packed word.  v_cvt_scalef32_* use the exponent field alone
 // (checked on gfx950: sign and fraction bits change nothing), so moving the

@@ -99,12 +99,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* p, i
 
 #endif
 
-// s_waitcnt vmcnt(N) with the other counters left alone.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
 #if defined(__HIP_DEVICE_COMPILE__)
