@@ -15,30 +15,48 @@ namespace kv {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
+constexpr int kPer = 4;  // requests per thread and turn
+constexpr int kTurn = kThreads * kPer;
 constexpr int kWavesB = kThreads / 64;
 
-// Inclusive sum over the work-group; *total gets the sum of all.
-template <class V>
-__device__ V block_scan(V x, V* scratch, V* total) {
+// Inclusive sums over a wave: within rows of 16 lanes, then from row to row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x = dpp_add<0x111, 0xf>(x);  // row_shr:1
+  x = dpp_add<0x112, 0xf>(x);
+  x = dpp_add<0x114, 0xf>(x);
+  x = dpp_add<0x118, 0xf>(x);
+  x = dpp_add<0x142, 0xa>(x);  // lane 15 of rows 0, 2 into rows 1, 3
+  return dpp_add<0x143, 0xc>(x);  // lane 31 into rows 2, 3
+}
+
+// Exclusive sums of N values over the work-group (32 bits within a wave) and
+// their totals.
+template <int N>
+__device__ __forceinline__ void block_scan(const uint32_t (&x)[N], int64_t (&before)[N], int64_t (&total)[N],
+                                           uint32_t (*scratch)[8]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t incl[N];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const V y = __shfl_up(x, d);
-    if (lane >= d) x += y;
+  for (int v = 0; v < N; ++v) {
+    incl[v] = wave_scan(x[v]);
+    if (lane == 63) scratch[wave][v] = incl[v];
   }
-  __syncthreads();  // scratch may still be read from the call before
-  if (lane == 63) scratch[wave] = x;
   __syncthreads();
-  V before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWavesB; ++w) {
-    const V s = scratch[w];
-    before += w < wave ? s : (V)0;
-    all += s;
+  for (int v = 0; v < N; ++v) {
+    before[v] = incl[v] - x[v];
+    total[v] = 0;
+#pragma unroll
+    for (int w = 0; w < kWavesB; ++w) {
+      if (w < wave) before[v] += scratch[w][v];
+      total[v] += scratch[w][v];
+    }
   }
-  *total = all;
-  return x + before;
 }
 
 // Largest i < n with start[i] <= x (start ascending, start[0] <= x).
@@ -60,92 +78,119 @@ __device__ __forceinline__ Request request(const BuildArgs& A, int i, int cap) {
   Request r{0, 0, 0, 0, false};
   if (i >= A.B) return r;
   const int c = A.ctx[i], n = A.add[i];
-  r.bad = c < 0 || n < 0 || c > cap || (int64_t)max(c, 0) + max(n, 0) > cap;
+  r.bad = c < 0 || n < 0 || (int64_t)max(c, 0) + max(n, 0) > cap;
   r.ctx = min(max(c, 0), cap);
-  r.add = max(n, 0);
+  r.add = min(max(n, 0), A.T);
   const int bt = 1 << A.bt_log2;
-  const int end = (int)min((int64_t)r.ctx + r.add, (int64_t)cap);
-  r.have = (r.ctx + bt - 1) >> A.bt_log2;
-  r.need = (int)(((int64_t)end + bt - 1) >> A.bt_log2);
+  const int64_t end = min((int64_t)r.ctx + r.add, (int64_t)cap);
+  r.have = (int)(((int64_t)r.ctx + bt - 1) >> A.bt_log2);
+  r.need = (int)((end + bt - 1) >> A.bt_log2);
   return r;
 }
 
-__device__ __forceinline__ int64_t tiles_of(int64_t tokens, int G) { return (tokens * G + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int tiles_of(int tokens, int G, int rows) {
+  return (int)(((int64_t)tokens * G + rows - 1) / rows);
+}
 
 __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
-  __shared__ int64_t scratch[kWavesB];
-  __shared__ int32_t scratch_i[kWavesB];
-  __shared__ int32_t s_row[kThreads];    // first token row
-  __shared__ int32_t s_fresh[kThreads];  // first new block, counted over the step
-  __shared__ int32_t s_item[kThreads];   // first work item
-  __shared__ int32_t s_wide[kThreads];   // first work item of 32 rows
-  __shared__ int32_t s_ctx[kThreads], s_chunks[kThreads], s_part[kThreads];
+  __shared__ uint32_t s_a[kWavesB][8], s_b[kWavesB][8];
+  __shared__ int64_t s_read[kWavesB];
+  __shared__ int32_t s_row[kTurn];    // first token row
+  __shared__ int32_t s_fresh[kTurn];  // first new block, counted over the step
+  __shared__ int32_t s_item[kTurn];   // first work item
+  __shared__ int32_t s_wide[kTurn];   // first work item of 32 rows
+  __shared__ int32_t s_ctx[kTurn], s_chunks[kTurn], s_part[kTurn];
   const int tid = threadIdx.x, wg = blockIdx.x, nwg = gridDim.x;
   const int bt = 1 << A.bt_log2;
   const int cap = (int)min((int64_t)A.width << A.bt_log2, (int64_t)0x7fffffff);
 
   // Tokens per work item, from the cached tokens that all row tiles read.
+  Request r[kPer];
   int64_t mine = 0;
-  for (int i = tid; i < A.B; i += kThreads) {
-    const Request r = request(A, i, cap);
-    mine += tiles_of(min(r.add, A.T), A.G) * min((int64_t)r.ctx + r.add, (int64_t)cap);
+  for (int base = 0; base < A.B; base += kTurn) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      r[e] = request(A, base + tid * kPer + e, cap);
+      mine += (int64_t)tiles_of(r[e].add, A.G, kUnit) * min((int64_t)r[e].ctx + r[e].add, (int64_t)cap);
+    }
   }
-  int64_t read;
-  block_scan<int64_t>(mine, scratch, &read);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) mine += __shfl_xor(mine, d);
+  if ((tid & 63) == 0) s_read[tid >> 6] = mine;
+  __syncthreads();
+  const int64_t read = s_read[0] + s_read[1] + s_read[2] + s_read[3];
   const int64_t per = (read * A.hkv + kTargetItems - 1) / kTargetItems;
   const int64_t rounded = max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)kMinChunk);
   const int chunk = (int)min(rounded, (int64_t)1 << 30);
 
   const bool wide_ok = wide_step(A.T, A.B);
-  int64_t rows0 = 0, fresh0 = 0;
-  int items0 = 0, wide0 = 0, parts0 = 0, flags = 0;
-  for (int base = 0; base < A.B; base += kThreads) {
-    const int i = base + tid;
-    const Request r = request(A, i, cap);
-    int64_t rows, fresh;
-    const int64_t row_end = rows0 + block_scan<int64_t>(r.add, scratch, &rows);
-    const int64_t fresh_end = fresh0 + block_scan<int64_t>(r.need - r.have, scratch, &fresh);
-    const int first = (int)min(row_end - r.add, (int64_t)A.T), last = (int)min(row_end, (int64_t)A.T);
-    const int64_t fresh_first = fresh_end - (r.need - r.have);
-    const int got = (int)max(min((int64_t)A.nfree - fresh_first, (int64_t)(r.need - r.have)), (int64_t)0);
-    const int kv = (int)min(min((int64_t)r.ctx + (last - first), (int64_t)cap), (int64_t)(r.have + got) << A.bt_log2);
-    const bool wide = wide_ok && (int64_t)(last - first) * A.G > kUnit;
-    const int tiles = (int)(((int64_t)(last - first) * A.G + (wide ? 2 * kUnit - 1 : kUnit - 1)) / (wide ? 2 * kUnit : kUnit));
-    const int chunks = max((kv + chunk - 1) / chunk, 1);
-    int items, wides, parts;
-    const int n_all = i < A.B ? tiles * chunks : 0;
-    const int n_items = wide ? 0 : n_all, n_wide = wide ? n_all : 0;
-    const int n_parts = chunks > 1 ? n_items + 2 * n_wide : 0;
-    const int item_end = items0 + block_scan<int32_t>(n_items, scratch_i, &items);
-    const int wide_end = wide0 + block_scan<int32_t>(n_wide, scratch_i, &wides);
-    const int part_end = parts0 + block_scan<int32_t>(n_parts, scratch_i, &parts);
-    s_row[tid] = first;
-    s_fresh[tid] = (int)min(fresh_first, (int64_t)0x7fffffff);
-    s_item[tid] = item_end - n_items;
-    s_wide[tid] = wide_end - n_wide;
-    s_ctx[tid] = r.ctx;
-    s_chunks[tid] = chunks;
-    s_part[tid] = chunks > 1 ? part_end - n_parts : -1;
-    if (wg == 0 && i < A.B) {
-      A.q_indptr[i] = first;
-      A.kv_len[i] = kv;
-      if (r.bad) flags |= LORA_KV_FLAG_LENGTH;
-      if (row_end > A.T) flags |= LORA_KV_FLAG_TOKENS;
-      if (fresh_end > A.nfree) flags |= LORA_KV_FLAG_FREE_LIST;
-      // the one cached block that new tokens may lie in
-      if (last > first && (r.ctx & (bt - 1)) != 0 &&
-          (unsigned)A.table[i * A.tstride + (r.ctx >> A.bt_log2)] >= (unsigned)A.blocks)
-        flags |= LORA_KV_FLAG_BLOCK_RANGE;
+  int64_t rows0 = 0, fresh0 = 0, items0 = 0, wide0 = 0, parts0 = 0;
+  int flags = 0;
+  for (int base = 0; base < A.B; base += kTurn) {
+    if (A.B > kTurn) {  // else the first pass left them here
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) r[e] = request(A, base + tid * kPer + e, cap);
+    }
+    uint32_t x[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[0] += r[e].add, x[1] += r[e].need - r[e].have;
+    int64_t at[2], sum[2];
+    block_scan<2>(x, at, sum, s_a);
+    int first[kPer], last[kPer], kv[kPer], n_items[kPer], n_wide[kPer], n_parts[kPer], chunks[kPer];
+    uint32_t y[3] = {0, 0, 0};
+    int64_t row = rows0 + at[0], fresh = fresh0 + at[1];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int i = base + tid * kPer + e, want = r[e].need - r[e].have;
+      first[e] = (int)min(row, (int64_t)A.T);
+      row += r[e].add;
+      last[e] = (int)min(row, (int64_t)A.T);
+      const int got = (int)max(min((int64_t)A.nfree - fresh, (int64_t)want), (int64_t)0);
+      s_fresh[tid * kPer + e] = (int)min(fresh, (int64_t)0x7fffffff);
+      fresh += want;
+      kv[e] = (int)min(min((int64_t)r[e].ctx + (last[e] - first[e]), (int64_t)cap), (int64_t)(r[e].have + got) << A.bt_log2);
+      const bool wide = wide_ok && (int64_t)(last[e] - first[e]) * A.G > kUnit;
+      chunks[e] = max((int)(((int64_t)kv[e] + chunk - 1) / chunk), 1);
+      const int n = i < A.B ? tiles_of(last[e] - first[e], A.G, wide ? 2 * kUnit : kUnit) * chunks[e] : 0;
+      n_items[e] = wide ? 0 : n;
+      n_wide[e] = wide ? n : 0;
+      n_parts[e] = chunks[e] > 1 ? n_items[e] + 2 * n_wide[e] : 0;
+      y[0] += n_items[e], y[1] += n_wide[e], y[2] += n_parts[e];
+      if (wg == 0 && i < A.B) {
+        A.q_indptr[i] = first[e];
+        A.kv_len[i] = kv[e];
+        if (r[e].bad) flags |= LORA_KV_FLAG_LENGTH;
+        if (row > A.T || A.add[i] > A.T) flags |= LORA_KV_FLAG_TOKENS;
+        if (want > 0 && fresh > A.nfree) flags |= LORA_KV_FLAG_FREE_LIST;
+        // the one cached block that new tokens may lie in
+        if (last[e] > first[e] && (r[e].ctx & (bt - 1)) != 0 &&
+            (unsigned)A.table[i * A.tstride + (r[e].ctx >> A.bt_log2)] >= (unsigned)A.blocks)
+          flags |= LORA_KV_FLAG_BLOCK_RANGE;
+      }
+    }
+    int64_t at2[3], sum2[3];
+    block_scan<3>(y, at2, sum2, s_b);
+    int64_t item = items0 + at2[0], wide = wide0 + at2[1], part = parts0 + at2[2];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int k = tid * kPer + e;
+      s_row[k] = first[e];
+      s_item[k] = (int)item;
+      s_wide[k] = (int)wide;
+      s_ctx[k] = r[e].ctx;
+      s_chunks[k] = chunks[e];
+      s_part[k] = chunks[e] > 1 ? (int)part : -1;
+      item += n_items[e], wide += n_wide[e], part += n_parts[e];
     }
     __syncthreads();
-    const int n = min(kThreads, A.B - base);
-    const int row0 = (int)min(rows0, (int64_t)A.T), row1 = (int)min(rows0 + rows, (int64_t)A.T);
+    const int n = min(kTurn, A.B - base);
+    const int row0 = (int)min(rows0, (int64_t)A.T), row1 = (int)min(rows0 + sum[0], (int64_t)A.T);
     for (int t = row0 + wg * kThreads + tid; t < row1; t += nwg * kThreads) {
       const int k = bisect(s_row, n, t);
       const int64_t pos = (int64_t)s_ctx[k] + (t - s_row[k]);
       int slot = -1;
       if (pos < cap) {
-        const int b = (int)(pos >> A.bt_log2), have = (s_ctx[k] + bt - 1) >> A.bt_log2;
+        const int b = (int)(pos >> A.bt_log2), have = (int)(((int64_t)s_ctx[k] + bt - 1) >> A.bt_log2);
         int id = -1;
         if (b < have) {
           id = A.table[(base + k) * A.tstride + b];
@@ -159,10 +204,10 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       A.positions[t] = (int)min(pos, (int64_t)0x7fffffff);
       A.slots[t] = slot;
     }
-    const int64_t fresh1 = min(fresh0 + fresh, (int64_t)0x7fffffff);
+    const int64_t fresh1 = min(fresh0 + sum[1], (int64_t)0x7fffffff);
     for (int64_t f = fresh0 + wg * kThreads + tid; f < fresh1; f += nwg * kThreads) {
       const int k = bisect(s_fresh, n, (int)f);
-      const int b = ((s_ctx[k] + bt - 1) >> A.bt_log2) + (int)(f - s_fresh[k]);
+      const int b = (int)(((int64_t)s_ctx[k] + bt - 1) >> A.bt_log2) + (int)(f - s_fresh[k]);
       int id = f < A.nfree ? A.free_blocks[f] : -1;
       if ((unsigned)id >= (unsigned)A.blocks) id = -1;
       A.table[(base + k) * A.tstride + b] = id;
@@ -184,15 +229,15 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       }
       *to = make_int4(base + k, tile, c, part);
     };
-    for (int w = items0 + wg * kThreads + tid; w < min(items0 + items, A.item_cap); w += nwg * kThreads)
+    for (int w = (int)items0 + wg * kThreads + tid; w < min(items0 + sum2[0], (int64_t)A.item_cap); w += nwg * kThreads)
       fill(s_item, w, 1, A.items + w);
-    for (int w = wide0 + wg * kThreads + tid; w < min(wide0 + wides, A.item_cap); w += nwg * kThreads)
+    for (int w = (int)wide0 + wg * kThreads + tid; w < min(wide0 + sum2[1], (int64_t)A.item_cap); w += nwg * kThreads)
       fill(s_wide, w, 2, A.items + A.item_cap + w);
-    rows0 += rows;
-    fresh0 += fresh;
-    items0 += items;
-    wide0 += wides;
-    parts0 += parts;
+    rows0 += sum[0];
+    fresh0 += sum[1];
+    items0 += sum2[0];
+    wide0 += sum2[1];
+    parts0 += sum2[2];
     __syncthreads();
   }
 
@@ -206,23 +251,22 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   if (wg == 0) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) flags |= __shfl_xor(flags, d);
-    __syncthreads();
-    if ((tid & 63) == 0) scratch_i[tid >> 6] = flags;
+    if ((tid & 63) == 0) s_a[tid >> 6][0] = (uint32_t)flags;
     __syncthreads();
     if (tid < kNumCounts) {
       int all = 0;
-      for (int w = 0; w < kWavesB; ++w) all |= scratch_i[w];
+      for (int w = 0; w < kWavesB; ++w) all |= (int)s_a[w][0];
       int v = 0;
       if (tid == kCountTokens) v = used;
       if (tid == kCountNewBlocks) v = (int)min(fresh0, (int64_t)0x7fffffff);
-      if (tid == kCountItems) v = items0;
-      if (tid == kCountParts) v = parts0;
-      if (tid == kCountWide) v = wide0;
+      if (tid == kCountItems) v = (int)items0;
+      if (tid == kCountParts) v = (int)parts0;
+      if (tid == kCountWide) v = (int)wide0;
       if (tid == kCountChunk) v = chunk;
       if (tid == kCountFlags) v = all;
       if (tid == kCountB) v = A.B;
       if (tid == kCountT) v = A.T;
-      if (tid == kCountCheck) v = check_word(A.B, A.T, items0, wide0, parts0);
+      if (tid == kCountCheck) v = check_word(A.B, A.T, (int)items0, (int)wide0, (int)parts0);
       A.counts[tid] = v;
     }
     if (tid == kThreads - 1) A.q_indptr[A.B] = used;
@@ -232,10 +276,9 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
 }  // namespace
 
 hipError_t launch_build(const BuildArgs& A, hipStream_t s) {
-  // one work-group per 1024 rows or 256 requests, up to 64: each repeats the
-  // sums over the requests
-  const int want = max_i(ceil_div_i(A.T, kThreads), ceil_div_i(A.B, 256));
-  const int grid = min_i(max_i(want, 1), 64);
+  // one work-group per 256 rows or requests, up to 128: each repeats the sums
+  // over the requests
+  const int grid = min_i(max_i(ceil_div_i(max_i(A.T, A.B), kThreads), 1), 128);
   build_kernel<<<grid, kThreads, 0, s>>>(A);
   return hipGetLastError();
 }

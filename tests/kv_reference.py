@@ -30,7 +30,8 @@ def build(ctx, new, T, table, free, num_blocks, bt):
     for i in range(B):
         if ctx[i] < 0 or new[i] < 0 or max(ctx[i], 0) + max(new[i], 0) > cap:
             flags |= 1
-        c, n = min(max(int(ctx[i]), 0), cap), max(int(new[i]), 0)
+        c, n = min(max(int(ctx[i]), 0), cap), min(max(int(new[i]), 0), T)
+        flags |= 2 * (new[i] > T)
         have, need = -(-c // bt), -(-min(c + n, cap) // bt)
         got = 0
         for b in range(have, need):
