@@ -276,9 +276,9 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
 }  // namespace
 
 hipError_t launch_build(const BuildArgs& A, hipStream_t s) {
-  // one work-group per 256 rows or requests, up to 128: each repeats the sums
+  // one work-group per 256 rows or requests, up to 512: each repeats the sums
   // over the requests
-  const int grid = min_i(max_i(ceil_div_i(max_i(A.T, A.B), kThreads), 1), 128);
+  const int grid = min_i(max_i(ceil_div_i(max_i(A.T, A.B), kThreads), 1), 512);
   build_kernel<<<grid, kThreads, 0, s>>>(A);
   return hipGetLastError();
 }

@@ -13,6 +13,7 @@ current stream, or on ``stream``.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -54,86 +55,99 @@ class lora_rope_t(ctypes.Structure):
 _bound = None
 
 
-def lib():
-    """liblora.so with this module's functions declared."""
+def lib() -> dict:
+    """liblora.so's attention functions by name, declared."""
     global _bound
     if _bound is None:
-        L, P = lora.lib(), ctypes.POINTER
-        heads, sz = P(lora_heads_t), ctypes.c_size_t
+        L, sz = lora.lib(), ctypes.c_size_t
         sigs = {
             "lora_kv_block_bytes": (sz, [_i32] * 3),
             "lora_kv_batch_size": (sz, [_i32] * 5),
-            "lora_kv_batch_init": (_i32, [_vp, sz] + [_i32] * 5 + [P(lora_kv_batch_t)]),
-            "lora_kv_build": (_i32, [_vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _i32, _i32, P(lora_kv_batch_t), _vp]),
-            "lora_rope_frequencies": (_i32, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, P(_f64)]),
-            "lora_rope": (_i32, [heads, heads, heads, heads, _vp, _i32, _i32, _i32, P(lora_rope_t), _vp]),
-            "lora_kv_append": (_i32, [heads, heads, heads, heads, _vp, _vp, _i32, _i32, P(lora_rope_t),
-                                      P(lora_kv_cache_t), _vp, _vp]),
-            "lora_kv_gather": (_i32, [P(lora_kv_cache_t), _vp, _i32, heads, heads, _i32, _vp]),
-            "lora_kv_workspace_size": (sz, [P(lora_kv_batch_t)]),
-            "lora_kv_attend": (_i32, [heads, heads, _i32, _i32, _i32, P(lora_kv_batch_t), _vp, _i64, _i32,
-                                      P(lora_kv_cache_t), ctypes.c_float, _vp, sz, _vp]),
-            "lora_prompt_attend": (_i32, [heads, heads, heads, heads, _vp, _i32, _i32, _i32, _i32, ctypes.c_float, _vp]),
+            "lora_kv_batch_init": (_i32, [_vp, sz] + [_i32] * 5 + [_vp]),
+            "lora_kv_build": (_i32, [_vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp, _vp]),
+            "lora_rope_frequencies": (_i32, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp]),
+            "lora_rope": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+            "lora_kv_append": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp]),
+            "lora_kv_gather": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+            "lora_kv_workspace_size": (sz, [_vp]),
+            "lora_kv_attend": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, ctypes.c_float, _vp, sz, _vp]),
+            "lora_prompt_attend": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_float, _vp]),
         }
+        fns = {}
         for name, (res, args) in sigs.items():
-            f = getattr(L, name)
+            fns[name] = f = getattr(L, name)
             f.restype, f.argtypes = res, args
-        _bound = L
+        _bound = fns
     return _bound
 
 
 # ------------------------------------------------------------------ checking
-def _heads(t: torch.Tensor, name: str) -> lora_heads_t:
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+# These run on every call of a decode step's many small launches, so they keep
+# to the cheapest accessors, and descriptors are packed bytes, not ctypes
+# structures.
+_pack_heads = struct.Struct("@Pqqi4x").pack  # lora_heads_t
+assert struct.calcsize("@Pqqi4x") == ctypes.sizeof(lora_heads_t)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_CODES = {torch.bfloat16: lora.LORA_DTYPE_BF16, torch.float32: lora.LORA_DTYPE_F32}
+
+
+def _heads(t: torch.Tensor, name: str, rows: int, dim: int, dtype: torch.dtype) -> bytes:
+    """Packed lora_heads_t of t (rows, heads, dim)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must have shape (tokens, heads, head_dim) with contiguous dims")
-    return lora_heads_t(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+    if shape[0] != rows:
+        raise ValueError(f"{name} has {shape[0]} rows, not {rows}")
+    if shape[2] != dim:
+        raise ValueError(f"{name} must have the call's head_dim {dim}, not {shape[2]}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has type {t.dtype}, not {dtype}")
+    return _pack_heads(t.data_ptr(), stride[0], stride[1], shape[1])
 
 
-def _ints(t: torch.Tensor, name: str, dim: int = 1) -> None:
-    if t.dtype != torch.int32 or t.dim() != dim or (t.numel() and t.stride(-1) != 1):
+def _code(dtype: torch.dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _ints(t: torch.Tensor, name: str, dim: int = 1) -> int:
+    """Address of an int32 tensor."""
+    if t.dtype != torch.int32 or t.dim() != dim or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be int32 with {dim} dimension(s), its last one contiguous")
+    return t.data_ptr()
 
 
-def _same_type(*named) -> int:
-    first = named[0][1].dtype
-    for name, t in named[1:]:
-        if t.dtype != first:
-            raise ValueError(f"{name} has type {t.dtype}, not {first}")
-    return lora.dtype_code(first)
-
-
-class _On:
-    """The device of a call's tensors, made current, and its stream."""
-
-    def __init__(self, stream, *tensors):
-        self.dev = dev = tensors[0].device
-        for t in tensors:
-            if t.device != dev:
-                raise ValueError(f"tensors of one call on {dev} and {t.device}")
-        if dev.type != "cuda":
-            raise ValueError(f"the attention operators need GPU tensors, got {dev}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
-        self.stream = stream
-
-    def call(self, name: str, *args) -> None:
-        if torch.cuda.current_device() == self.dev.index:
-            st = self._run(name, args)
-        else:
-            with torch.cuda.device(self.dev):
-                st = self._run(name, args)
-        if st != 0:
-            raise lora.LoraError(name, st)
-
-    def _run(self, name, args):
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
-        return getattr(lib(), name)(*args, s.cuda_stream)
+def _call(name: str, stream, tensors, *args) -> None:
+    """The C call on the tensors' device and its current stream (or `stream`)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: tensors of one call on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"{name} needs GPU tensors")
+    if stream is None:
+        s = _raw_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{name}: a stream of {stream.device} for tensors on {tensors[0].device}")
+    else:
+        s = stream.cuda_stream
+    fn = (_bound or lib())[name]
+    if _current() == dev:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise lora.LoraError(name, st)
 
 
 # ------------------------------------------------------------------ handles
 def block_bytes(block_tokens: int, num_kv_heads: int, head_dim: int) -> int:
     """Bytes of one cache block (0: unsupported geometry)."""
-    return int(lib().lora_kv_block_bytes(block_tokens, num_kv_heads, head_dim))
+    return int(lib()["lora_kv_block_bytes"](block_tokens, num_kv_heads, head_dim))
 
 
 class Cache:
@@ -150,7 +164,7 @@ class Cache:
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
         stride = data.stride(0) if data.shape[0] > 1 else max(data.stride(0), need)
         self.c = lora_kv_cache_t(data.data_ptr(), stride, data.shape[0], block_tokens, num_kv_heads, head_dim)
-        self.ref = ctypes.byref(self.c)
+        self.ref = ctypes.addressof(self.c)
 
     @classmethod
     def in_pool(cls, pool: "lora.Pool", block_tokens: int, num_kv_heads: int, head_dim: int) -> "Cache":
@@ -168,7 +182,7 @@ class Rope:
             raise ValueError("inv_freq must be a contiguous float64 vector")
         self.inv_freq, self.rot_dim, self.layout, self.scale = inv_freq, 2 * inv_freq.numel(), layout, scale
         self.c = lora_rope_t(inv_freq.data_ptr(), self.rot_dim, layout, scale)
-        self.ref = ctypes.byref(self.c)
+        self.ref = ctypes.addressof(self.c)
 
     @classmethod
     def scaled(cls, rot_dim: int, theta: float = 10000.0, scaling: int = SCALING_NONE, factor: float = 1.0,
@@ -185,38 +199,38 @@ class Batch:
     def __init__(self, max_tokens: int, max_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  device="cuda"):
         L = lib()
-        n = L.lora_kv_batch_size(max_tokens, max_seqs, num_q_heads, num_kv_heads, head_dim)
+        n = L["lora_kv_batch_size"](max_tokens, max_seqs, num_q_heads, num_kv_heads, head_dim)
         if n == 0:
             raise ValueError("unsupported batch capacity or head geometry")
         # zeroed: a buffer that was never built must not look like one that was
         self.buf = torch.zeros(n, dtype=torch.uint8, device=device)
         self.c = lora_kv_batch_t()
-        self.ref = ctypes.byref(self.c)
-        st = L.lora_kv_batch_init(self.buf.data_ptr(), n, max_tokens, max_seqs, num_q_heads, num_kv_heads, head_dim, self.ref)
+        self.ref = ctypes.addressof(self.c)
+        st = L["lora_kv_batch_init"](self.buf.data_ptr(), n, max_tokens, max_seqs, num_q_heads, num_kv_heads, head_dim, self.ref)
         if st != 0:
             raise lora.LoraError("lora_kv_batch_init", st)
-        self.T = self.B = 0  # of the last build
         self._all = {name: self._view(name, size) for name, size in
                      (("q_indptr", max_seqs + 1), ("kv_len", max_seqs), ("token_seq", max_tokens),
                       ("positions", max_tokens), ("slots", max_tokens), ("counts", N_COUNTS))}
+        self.counts = self._all["counts"]
+        self.flags = self.counts[COUNT_FLAGS:COUNT_FLAGS + 1]
+        self.new_blocks = self.counts[COUNT_NEW_BLOCKS:COUNT_NEW_BLOCKS + 1]
+        self._resize(0, 0)
 
     def _view(self, field: str, n: int) -> torch.Tensor:
         off = getattr(self.c, field) - self.buf.data_ptr()
         return self.buf[off:off + 4 * n].view(torch.int32)
 
-    q_indptr = property(lambda self: self._all["q_indptr"][:self.B + 1])
-    kv_len = property(lambda self: self._all["kv_len"][:self.B])
-    token_seq = property(lambda self: self._all["token_seq"][:self.T])
-    positions = property(lambda self: self._all["positions"][:self.T])
-    slots = property(lambda self: self._all["slots"][:self.T])
-    counts = property(lambda self: self._all["counts"])
-    flags = property(lambda self: self._all["counts"][COUNT_FLAGS:COUNT_FLAGS + 1])
-    new_blocks = property(lambda self: self._all["counts"][COUNT_NEW_BLOCKS:COUNT_NEW_BLOCKS + 1])
+    def _resize(self, T: int, B: int) -> None:
+        """The arrays' views for a build of T rows and B requests."""
+        self.T, self.B = T, B
+        self.q_indptr, self.kv_len = self._all["q_indptr"][:B + 1], self._all["kv_len"][:B]
+        self.token_seq, self.positions, self.slots = (self._all[n][:T] for n in ("token_seq", "positions", "slots"))
 
 
 def attend_workspace(batch: Batch) -> torch.Tensor:
     """Workspace of lora_kv_attend for a batch buffer (one serves every layer)."""
-    n = lib().lora_kv_workspace_size(batch.ref)
+    n = lib()["lora_kv_workspace_size"](batch.ref)
     return torch.empty(n, dtype=torch.uint8, device=batch.buf.device)
 
 
@@ -225,7 +239,7 @@ def lora_rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = S
                           original: float = 0.0, low: float = 0.0, high: float = 0.0):
     """(frequencies as a list of floats, scale of cos and sin)."""
     out, scale = (_f64 * max(rot_dim // 2, 1))(), _f64()
-    st = lib().lora_rope_frequencies(rot_dim, theta, scaling, factor, original, low, high, out, ctypes.byref(scale))
+    st = lib()["lora_rope_frequencies"](rot_dim, theta, scaling, factor, original, low, high, out, ctypes.byref(scale))
     if st != 0:
         raise lora.LoraError("lora_rope_frequencies", st)
     return list(out), scale.value
@@ -235,40 +249,32 @@ def lora_kv_build(ctx_len: torch.Tensor, new_len: torch.Tensor, T: int, block_ta
                   free_blocks: torch.Tensor, num_blocks: int, block_tokens: int, batch: Batch, stream=None) -> None:
     """Rows, positions, slots and plan of a step from request lengths; new
     blocks go from free_blocks into block_table (B, width)."""
-    _ints(ctx_len, "ctx_len"), _ints(new_len, "new_len"), _ints(free_blocks, "free_blocks")
-    _ints(block_table, "block_table", 2)
-    B = ctx_len.numel()
-    if new_len.numel() != B or block_table.shape[0] != B:
+    B, width = ctx_len.shape[0], block_table.shape[-1]
+    if new_len.shape[0] != B or block_table.shape[0] != B:
         raise ValueError("one length of each kind and one table row per request")
-    on = _On(stream, ctx_len, new_len, block_table, free_blocks, batch.buf)
-    on.call("lora_kv_build", ctx_len.data_ptr(), new_len.data_ptr(), B, T, block_table.data_ptr(),
-            max(block_table.stride(0), block_table.shape[1]), block_table.shape[1], free_blocks.data_ptr(),
-            free_blocks.numel(), num_blocks, block_tokens, batch.ref)
-    batch.T, batch.B = T, B
-
-
-def _rows(name: str, t: torch.Tensor, n: int) -> None:
-    if t.shape[0] != n:
-        raise ValueError(f"{name} has {t.shape[0]} rows, not {n}")
+    _call("lora_kv_build", stream, (ctx_len, new_len, block_table, free_blocks, batch.buf),
+          _ints(ctx_len, "ctx_len"), _ints(new_len, "new_len"), B, T, _ints(block_table, "block_table", 2),
+          max(block_table.stride(0), width), width, _ints(free_blocks, "free_blocks"), free_blocks.shape[0], num_blocks,
+          block_tokens, batch.ref)
+    if batch.T != T or batch.B != B:
+        batch._resize(T, B)
 
 
 def lora_rope(q: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k: Optional[torch.Tensor],
               k_out: Optional[torch.Tensor], positions: torch.Tensor, rope: Rope, stream=None) -> None:
     """Rotate q and k (T, heads, head_dim; either may be None) into q_out and
     k_out, which may be q and k."""
-    _ints(positions, "positions")
-    named = [(n, t) for n, t in (("q", q), ("q_out", q_out), ("k", k), ("k_out", k_out)) if t is not None]
-    if not named or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+    if (q is None and k is None) or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q with q_out, k with k_out, or both")
-    T, D = positions.numel(), named[0][1].shape[2]
-    code = _same_type(*named)
-    for n, t in named:
-        _rows(n, t, T)
-        if t.dim() != 3 or t.shape[2] != D:
-            raise ValueError("q and k must have the same head_dim")
-    ref = [None if t is None else ctypes.byref(_heads(t, n)) for n, t in (("q", q), ("q_out", q_out), ("k", k), ("k_out", k_out))]
-    on = _On(stream, positions, rope.inv_freq, *(t for _, t in named))
-    on.call("lora_rope", *ref, positions.data_ptr(), T, D, code, rope.ref)
+    pos, T = _ints(positions, "positions"), positions.shape[0]
+    lead = k if q is None else q
+    D, dtype = lead.shape[-1], lead.dtype
+    tensors, ref = [positions, rope.inv_freq], []
+    for name, t in (("q", q), ("q_out", q_out), ("k", k), ("k_out", k_out)):
+        ref.append(None if t is None else _heads(t, name, T, D, dtype))
+        if t is not None:
+            tensors.append(t)
+    _call("lora_rope", stream, tensors, *ref, pos, T, D, _code(dtype), rope.ref)
 
 
 def lora_kv_append(q: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -276,80 +282,60 @@ def lora_kv_append(q: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k: 
                    batch: Optional[Batch] = None, stream=None) -> None:
     """Rotate q into q_out and put rotated k, and v, into the cache at slots.
     rope None: no rotation.  batch: whose flags take FLAG_NONFINITE."""
-    _ints(slots, "slots")
-    T = slots.numel()
+    slot, T = _ints(slots, "slots"), slots.shape[0]
     if rope is None and q is not None:
         raise ValueError("q is only rotated: pass rope, or no q")
     if rope is not None and positions is None:
         raise ValueError("rope needs positions")
     if (q is None) != (q_out is None):
         raise ValueError("q with q_out")
+    D, dtype = cache.head_dim, k.dtype
     tensors = [slots, cache.data, k, v]
-    named = [("k", k), ("v", v)]
+    kr, vr = _heads(k, "k", T, D, dtype), _heads(v, "v", T, D, dtype)
+    qr = qo = pos = flags = None
     if q is not None:
-        named += [("q", q), ("q_out", q_out)]
-        tensors += [q, q_out]
+        qr, qo = _heads(q, "q", T, D, dtype), _heads(q_out, "q_out", T, D, dtype)
+        tensors += (q, q_out)
     if positions is not None:
-        _ints(positions, "positions")
-        _rows("positions", positions, T)
+        pos = _ints(positions, "positions")
+        if positions.shape[0] != T:
+            raise ValueError("one position per slot")
         tensors.append(positions)
     if rope is not None:
         tensors.append(rope.inv_freq)
-    code = _same_type(*named)
-    for n, t in named:
-        _rows(n, t, T)
-        if t.dim() != 3 or t.shape[2] != cache.head_dim:
-            raise ValueError(f"{n} must have the cache's head_dim {cache.head_dim}")
-    on = _On(stream, *tensors)
-    ref = lambda t, n: None if t is None else ctypes.byref(_heads(t, n))  # noqa: E731
-    on.call("lora_kv_append", ref(q, "q"), ref(q_out, "q_out"), ref(k, "k"), ref(v, "v"),
-            None if positions is None else positions.data_ptr(), slots.data_ptr(), T, code,
-            None if rope is None else rope.ref, cache.ref, None if batch is None else batch.flags.data_ptr())
+    if batch is not None:
+        flags = batch.c.counts + 4 * COUNT_FLAGS
+        tensors.append(batch.buf)
+    _call("lora_kv_append", stream, tensors, qr, qo, kr, vr, pos, slot, T, _code(dtype),
+          None if rope is None else rope.ref, cache.ref, flags)
 
 
 def lora_kv_gather(cache: Cache, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None) -> None:
     """The cached K and V at slots as values (n, kv heads, head_dim)."""
-    _ints(slots, "slots")
-    n = slots.numel()
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _rows(name, t, n)
-        if t.dim() != 3 or t.shape[2] != cache.head_dim:
-            raise ValueError(f"{name} must have the cache's head_dim {cache.head_dim}")
-    code = _same_type(("k_out", k_out), ("v_out", v_out))
-    on = _On(stream, slots, cache.data, k_out, v_out)
-    on.call("lora_kv_gather", cache.ref, slots.data_ptr(), n, ctypes.byref(_heads(k_out, "k_out")),
-            ctypes.byref(_heads(v_out, "v_out")), code)
+    slot, n, dtype = _ints(slots, "slots"), slots.shape[0], k_out.dtype
+    _call("lora_kv_gather", stream, (slots, cache.data, k_out, v_out), cache.ref, slot, n,
+          _heads(k_out, "k_out", n, cache.head_dim, dtype), _heads(v_out, "v_out", n, cache.head_dim, dtype), _code(dtype))
 
 
 def lora_kv_attend(q: torch.Tensor, out: torch.Tensor, batch: Batch, block_table: torch.Tensor, cache: Cache,
                    scale: float, ws: torch.Tensor, stream=None) -> None:
     """Attention of the batch's rows q (T, heads, head_dim) over the cache."""
-    _ints(block_table, "block_table", 2)
-    for name, t in (("q", q), ("out", out)):
-        _rows(name, t, batch.T)
-        if t.dim() != 3 or t.shape[2] != cache.head_dim:
-            raise ValueError(f"{name} must have the cache's head_dim {cache.head_dim}")
-    _rows("block_table", block_table, batch.B)
-    code = _same_type(("q", q), ("out", out))
-    on = _On(stream, q, out, batch.buf, block_table, cache.data, ws)
-    on.call("lora_kv_attend", ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(out, "out")), batch.T, batch.B, code,
-            batch.ref, block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
-            cache.ref, scale, ws.data_ptr(), ws.numel() * ws.element_size())
+    table, width, dtype = _ints(block_table, "block_table", 2), block_table.shape[1], q.dtype
+    if block_table.shape[0] != batch.B:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows, not {batch.B}")
+    _call("lora_kv_attend", stream, (q, out, batch.buf, block_table, cache.data, ws),
+          _heads(q, "q", batch.T, cache.head_dim, dtype), _heads(out, "out", batch.T, cache.head_dim, dtype), batch.T, batch.B,
+          _code(dtype), batch.ref, table, max(block_table.stride(0), width), width, cache.ref, scale, ws.data_ptr(),
+          ws.numel() * ws.element_size())
 
 
 def lora_prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, indptr: torch.Tensor,
                        scale: float, stream=None) -> None:
     """Causal attention of packed prompts: rows indptr[i]..indptr[i+1]-1 of q,
     k, v and out (T, heads, head_dim) are prompt i."""
-    _ints(indptr, "indptr")
-    if indptr.numel() < 1:
+    ptr, B = _ints(indptr, "indptr"), indptr.shape[0] - 1
+    if B < 0:
         raise ValueError("indptr has one entry more than prompts")
-    T = q.shape[0]
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _rows(name, t, T)
-        if t.dim() != 3 or t.shape[2] != q.shape[2]:
-            raise ValueError("q, k, v and out must have the same head_dim")
-    code = _same_type(("q", q), ("k", k), ("v", v), ("out", out))
-    on = _On(stream, q, k, v, out, indptr)
-    on.call("lora_prompt_attend", *(ctypes.byref(_heads(t, n)) for n, t in (("q", q), ("k", k), ("v", v), ("out", out))),
-            indptr.data_ptr(), indptr.numel() - 1, T, q.shape[2], code, scale)
+    T, D, dtype = q.shape[0], q.shape[-1], q.dtype
+    _call("lora_prompt_attend", stream, (q, k, v, out, indptr), _heads(q, "q", T, D, dtype), _heads(k, "k", T, D, dtype),
+          _heads(v, "v", T, D, dtype), _heads(out, "out", T, D, dtype), ptr, B, T, D, _code(dtype), scale)
