@@ -44,6 +44,18 @@ __device__ __forceinline__ void from_f(float* p, float f) { *p = f; }
 __device__ __forceinline__ float round_to(float f, Bf16) { return bf_to_f(f_to_bf(f)); }
 __device__ __forceinline__ float round_to(float f, F32) { return f; }
 
+__device__ __forceinline__ void unpack(u32x4 w, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack(u32x4 w, float (&x)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(w[j]);
+}
+
 // N (a multiple of the vector width) consecutive elements at a 16-byte
 // aligned address.
 template <int N>

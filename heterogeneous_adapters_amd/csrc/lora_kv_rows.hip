@@ -38,67 +38,112 @@ __device__ __forceinline__ double2 angle(const RopeArgs& A, int pos, int pair) {
 }
 
 // ------------------------------------------------------------ rotation role
-// V: arithmetic type.  One task = one vector of pairs, or one vector of dims
-// behind rot_dim (copied when out of place).
-template <class E, class V, class V2>
+// Quotient by a small run-time divisor: n * d < 2^32 here, where m = ceil(2^32
+// / d) gives it exactly.
+struct Div {
+  uint32_t m;
+  __device__ explicit Div(int d) : m(d > 1 ? 0xffffffffu / (uint32_t)d + 1 : 0) {}
+  __device__ __forceinline__ int operator()(int n) const { return m ? (int)__umulhi((uint32_t)n, m) : n; }
+};
+
+// Heads h0 .. h0+nh-1 of `in` into `out` for nt tokens.  V: arithmetic type.
+// One task = one vector of pairs, or one vector of dims behind rot_dim (copied
+// when out of place).  `angles` fills cs and is called once the first turn's
+// loads are on their way.
+template <class E, class V, class V2, class F>
 __device__ __forceinline__ void rotate_heads(const RopeArgs& A, const Rows& in, const Rows& out, int t0, int nt, int h0,
-                                             int nh, const V2* cs, int cs_stride) {
+                                             int nh, const V2* cs, F&& angles) {
   typedef typename E::T T;
   constexpr int EPV = E::kEpv;
+  constexpr int U = 4;  // tasks in flight per thread
   const int half = A.rot >> 1;
-  const bool copy = in.p != out.p;
-  const bool wide = A.interleaved ? A.rot % EPV == 0 : half % EPV == 0;
-  const int pair_tasks = wide ? (A.interleaved ? A.rot / EPV : half / EPV) : half;
+  const bool copy = in.p != out.p, inter = A.interleaved != 0;
+  const bool wide = inter ? A.rot % EPV == 0 : half % EPV == 0;
   const int tail = copy ? A.D - A.rot : 0;
   const bool tail_wide = A.rot % EPV == 0;
+  const int pair_tasks = wide ? (inter ? A.rot / EPV : half / EPV) : half;
   const int per_head = pair_tasks + (tail_wide ? tail / EPV : tail);
   const int total = nt * nh * per_head;
-  for (int idx = threadIdx.x; idx < total; idx += kThreads) {
-    const int th = idx / per_head, task = idx - th * per_head;
-    const int tl = th / nh, h = h0 + th - tl * nh, t = t0 + tl;
+  const Div by_head(per_head), by_token(nh);
+  if (wide && tail_wide) {
+    for (int base = 0; base < total; base += U * kThreads) {
+      u32x4 a[U], b[U];
+      T* y[U];
+      int at[U];  // first dim; -1: nothing to do; + kMaxPairs * 4: a copy
+      int tl[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int idx = base + u * kThreads + threadIdx.x;
+        at[u] = -1;
+        if (idx >= total) continue;
+        const int th = by_head(idx), task = idx - th * per_head, h = th - by_token(th) * nh + h0;
+        tl[u] = by_token(th);
+        const int t = t0 + tl[u];
+        if (A.pos[t] < 0) continue;
+        const bool pass = task >= pair_tasks;
+        const int d = pass ? A.rot + (task - pair_tasks) * EPV : task * EPV;
+        const T* x = static_cast<const T*>(in.p) + t * in.ts + h * in.hs + d;
+        y[u] = static_cast<T*>(out.p) + t * out.ts + h * out.hs + d;
+        at[u] = pass ? d + 4 * kMaxPairs : d;
+        a[u] = *reinterpret_cast<const u32x4*>(x);
+        if (!inter && !pass) b[u] = *reinterpret_cast<const u32x4*>(x + half);
+      }
+      if (base == 0) angles();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (at[u] < 0) continue;
+        if (at[u] >= 4 * kMaxPairs) {
+          *reinterpret_cast<u32x4*>(y[u]) = a[u];
+          continue;
+        }
+        const V2* w = cs + tl[u] * half;
+        float xa[EPV], xb[EPV], r[EPV], s[EPV];
+        unpack(a[u], xa);
+        if (inter) {
+          w += at[u] / 2;
+#pragma unroll
+          for (int i = 0; i < EPV / 2; ++i) {
+            const V p = xa[2 * i], q = xa[2 * i + 1];
+            r[2 * i] = (float)(p * w[i].x - q * w[i].y);
+            r[2 * i + 1] = (float)(q * w[i].x + p * w[i].y);
+          }
+          store_n<EPV>(y[u], r);
+        } else {
+          unpack(b[u], xb);
+          w += at[u];
+#pragma unroll
+          for (int i = 0; i < EPV; ++i) {
+            const V p = xa[i], q = xb[i];
+            r[i] = (float)(p * w[i].x - q * w[i].y);
+            s[i] = (float)(q * w[i].x + p * w[i].y);
+          }
+          store_n<EPV>(y[u], r);
+          store_n<EPV>(y[u] + half, s);
+        }
+      }
+    }
+    return;
+  }
+  angles();
+  for (int idx = threadIdx.x; idx < total; idx += kThreads) {  // rot_dim not in whole vectors
+    const int th = by_head(idx), task = idx - th * per_head;
+    const int tl = by_token(th), h = h0 + th - tl * nh, t = t0 + tl;
     if (A.pos[t] < 0) continue;
     const T* x = static_cast<const T*>(in.p) + t * in.ts + h * in.hs;
     T* y = static_cast<T*>(out.p) + t * out.ts + h * out.hs;
-    const V2* cst = cs + tl * cs_stride;
+    const V2* w = cs + tl * half;
+    const int n = task < pair_tasks ? (wide ? EPV : 1) : (tail_wide ? EPV : 1);
     if (task >= pair_tasks) {
-      if (tail_wide) {
-        const int d = A.rot + (task - pair_tasks) * EPV;
-        *reinterpret_cast<u32x4*>(y + d) = *reinterpret_cast<const u32x4*>(x + d);
-      } else {
-        const int d = A.rot + task - pair_tasks;
-        y[d] = x[d];
-      }
-    } else if (!wide) {
-      const int d0 = A.interleaved ? 2 * task : task, d1 = A.interleaved ? d0 + 1 : task + half;
-      const V a = to_f(x[d0]), b = to_f(x[d1]);
-      from_f(y + d0, (float)(a * cst[task].x - b * cst[task].y));
-      from_f(y + d1, (float)(b * cst[task].x + a * cst[task].y));
-    } else if (A.interleaved) {
-      const int d = task * EPV;
-      float a[EPV], r[EPV];
-      load_n<EPV>(x + d, a);
-#pragma unroll
-      for (int i = 0; i < EPV / 2; ++i) {
-        const V2 w = cst[d / 2 + i];
-        const V u = a[2 * i], v = a[2 * i + 1];
-        r[2 * i] = (float)(u * w.x - v * w.y);
-        r[2 * i + 1] = (float)(v * w.x + u * w.y);
-      }
-      store_n<EPV>(y + d, r);
-    } else {
-      const int d = task * EPV;
-      float a[EPV], b[EPV], r[EPV], s[EPV];
-      load_n<EPV>(x + d, a);
-      load_n<EPV>(x + d + half, b);
-#pragma unroll
-      for (int i = 0; i < EPV; ++i) {
-        const V2 w = cst[d + i];
-        const V u = a[i], v = b[i];
-        r[i] = (float)(u * w.x - v * w.y);
-        s[i] = (float)(v * w.x + u * w.y);
-      }
-      store_n<EPV>(y + d, r);
-      store_n<EPV>(y + d + half, s);
+      const int d = A.rot + (task - pair_tasks) * n;
+      for (int i = 0; i < n; ++i) y[d + i] = x[d + i];
+      continue;
+    }
+    for (int i = 0; i < (wide && inter ? n / 2 : n); ++i) {
+      const int pair = wide ? (inter ? task * EPV / 2 : task * EPV) + i : task;
+      const int d0 = inter ? 2 * pair : pair, d1 = inter ? d0 + 1 : pair + half;
+      const V p = to_f(x[d0]), q = to_f(x[d1]);
+      from_f(y + d0, (float)(p * w[pair].x - q * w[pair].y));
+      from_f(y + d1, (float)(q * w[pair].x + p * w[pair].y));
     }
   }
 }
@@ -109,33 +154,39 @@ __device__ __forceinline__ void rotate_role(const RopeArgs& A, int block, double
   const int half = A.rot >> 1;
   const int t0 = block / A.q_groups * kRotTokens, g = block % A.q_groups;
   const int nt = min(kRotTokens, A.T - t0);
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int tl = i / half, pair = i - tl * half, p = A.pos[t0 + tl];
-    if (p < 0) continue;
-    const double2 w = angle(A, p, pair);
-    lds[tl * half + pair] = w;
-    lf[tl * half + pair] = make_float2((float)w.x, (float)w.y);
-  }
-  __syncthreads();
+  auto angles = [&]() {
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+      const int tl = i / half, p = A.pos[t0 + tl];
+      if (p < 0) continue;
+      const double2 w = angle(A, p, i - tl * half);
+      lds[i] = w;
+      lf[i] = make_float2((float)w.x, (float)w.y);
+    }
+    __syncthreads();
+  };
   // heads of q, then of k
   const int lo = g * A.q_heads_per_group, hi = min(lo + A.q_heads_per_group, A.qo.heads + A.ko.heads);
   const int nq = min(hi, A.qo.heads) - min(lo, A.qo.heads), nk = hi - lo - nq;
-  if (nq > 0) rotate_heads<E, float>(A, A.q, A.qo, t0, nt, lo, nq, lf, half);
-  if (nk > 0) rotate_heads<E, double>(A, A.k, A.ko, t0, nt, max(lo - A.qo.heads, 0), nk, lds, half);
+  if (nq > 0) rotate_heads<E, float>(A, A.q, A.qo, t0, nt, lo, nq, lf, angles);
+  if (nk > 0) {
+    const int h0 = max(lo - A.qo.heads, 0);
+    if (nq > 0) rotate_heads<E, double>(A, A.k, A.ko, t0, nt, h0, nk, lds, [] {});
+    else rotate_heads<E, double>(A, A.k, A.ko, t0, nt, h0, nk, lds, angles);
+  }
 }
 
 // --------------------------------------------------------------- cache role
-// 32 dims of one head as rounded, rotated values.
+// Eight dims of one head, from dim d0 on, as rounded, rotated values.
 template <class E, bool ROPE>
-__device__ __forceinline__ void load_group(const RopeArgs& A, const typename E::T* x, int c, const double2* cs,
-                                           float (&f)[32]) {
-  load_n<32>(x + 32 * c, f);
+__device__ __forceinline__ void load_eight(const RopeArgs& A, const typename E::T* x, int d0, const double2* cs,
+                                           float (&f)[8]) {
+  load_n<8>(x + d0, f);
   if constexpr (!ROPE) return;
-  const int half = A.rot >> 1, d0 = 32 * c;
+  const int half = A.rot >> 1;
   if (d0 >= A.rot) return;
   if (A.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (d0 + 2 * i < A.rot) {
         const double2 w = cs[d0 / 2 + i];
         const double u = f[2 * i], v = f[2 * i + 1];
@@ -144,24 +195,18 @@ __device__ __forceinline__ void load_group(const RopeArgs& A, const typename E::
       }
     }
   } else if (half % 8 == 0) {
+    const bool low = d0 < half;
+    const double2* w = cs + (low ? d0 : d0 - half);
+    float o[8];
+    load_n<8>(x + (low ? d0 + half : d0 - half), o);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int d = d0 + 8 * v;
-      if (d >= A.rot) continue;
-      const bool low = d < half;
-      const int pair = low ? d : d - half;
-      float o[8];
-      load_n<8>(x + (low ? d + half : d - half), o);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double2 w = cs[pair + i];
-        const double a = f[8 * v + i], b = o[i];
-        f[8 * v + i] = round_to((float)(low ? a * w.x - b * w.y : a * w.x + b * w.y), E{});
-      }
+    for (int i = 0; i < 8; ++i) {
+      const double a = f[i], b = low ? -o[i] : o[i];
+      f[i] = round_to((float)(a * w[i].x + b * w[i].y), E{});
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int d = d0 + i;
       if (d >= A.rot) continue;
       const bool low = d < half;
@@ -172,21 +217,24 @@ __device__ __forceinline__ void load_group(const RopeArgs& A, const typename E::
   }
 }
 
-// Scale byte of a group; NaN become 0.  Returns whether all were finite.
-__device__ __forceinline__ bool scale_byte(float (&f)[32], int& byte) {
+// Largest finite magnitude; NaN become 0.  Clears `fine` unless all are finite.
+template <int N>
+__device__ __forceinline__ float magnitude(float (&f)[N], bool& fine) {
   float most = 0.0f;
-  bool fine = true;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < N; ++i) {
     const float a = fabsf(f[i]);
     const bool finite = a <= 3.402823466e38f;
     most = fmaxf(most, finite ? a : 0.0f);
     fine = fine && finite;
     if (f[i] != f[i]) f[i] = 0.0f;
   }
+  return most;
+}
+// Scale byte of a group: 2^e with the least e with most <= 7 * 2^e.
+__device__ __forceinline__ int scale_byte(float most) {
   const int e = (int)((__float_as_uint(most) + 0x1fffffu) >> 23) - 2;
-  byte = min(max(e, 32), 251);
-  return fine;
+  return min(max(e, 32), 251);
 }
 
 __device__ __forceinline__ uint32_t encode8(float a0, float b0, float a1, float b1, float a2, float b2, float a3,
@@ -199,10 +247,15 @@ __device__ __forceinline__ uint32_t encode8(float a0, float b0, float a1, float 
   return w;
 }
 
-// Value of lane j of each group of four lanes.
-template <int J>
+// Values of the other lanes of each group of four: CTRL names, for lanes 0 to
+// 3, the lane to read (two bits each).
+template <int CTRL>
 __device__ __forceinline__ uint32_t quad(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, J * 0x55, 0xf, 0xf, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, false);
+}
+template <int J>
+__device__ __forceinline__ uint32_t quad_lane(uint32_t x) {
+  return quad<J * 0x55>(x);
 }
 
 __device__ __forceinline__ uint8_t* record(const Cache& C, int slot, int h) {
@@ -211,56 +264,75 @@ __device__ __forceinline__ uint8_t* record(const Cache& C, int slot, int h) {
 }
 
 template <class E, bool ROPE>
-__device__ __forceinline__ void cache_role(const RopeArgs& A, int block, double2* cs) {
+__device__ __forceinline__ void cache_role(const RopeArgs& A, int block, double2* cs, int* s_slot) {
+  typedef typename E::T T;
   const Cache& C = A.cache;
   const int nc = C.nc, half = A.rot >> 1;
   const int t0 = block / A.kv_groups * kCacheTokens, g = block % A.kv_groups;
   const int nt = min(kCacheTokens, A.T - t0);
+  const int h_first = g * A.kv_heads_per_group, h_end = min(h_first + A.kv_heads_per_group, C.heads);
+  if (threadIdx.x < kCacheTokens) {
+    int slot = -1;
+    if ((int)threadIdx.x < nt) {
+      slot = A.slots[t0 + threadIdx.x];
+      if ((unsigned)(slot >> C.bt_log2) >= (unsigned)C.blocks) slot = -1;
+      if (ROPE && A.pos[t0 + threadIdx.x] < 0) slot = -1;
+    }
+    s_slot[threadIdx.x] = slot;
+  }
   if constexpr (ROPE) {
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
       const int tl = i / half, p = A.pos[t0 + tl];
       if (p >= 0) cs[i] = angle(A, p, i - tl * half);
     }
-    __syncthreads();
   }
-  // lane quads hold 4 consecutive tokens of one (head, group): (t/4, c, t%4)
+  __syncthreads();
+  bool fine = true;
+
+  // K: four lanes per group of 32, eight dims and one word of codes each
+  {
+    const int per_token = 4 * nc, per_head = kCacheTokens * per_token, total = (h_end - h_first) * per_head;
+    const Div by_head(per_head), by_token(per_token);
+    for (int idx = threadIdx.x; idx < total; idx += kThreads) {
+      const int hl = by_head(idx), r = idx - hl * per_head, tl = by_token(r), cv = r - tl * per_token;
+      const int slot = s_slot[tl];
+      if (slot < 0) continue;  // the same for the four lanes
+      const int h = h_first + hl, t = t0 + tl, c = cv >> 2, v = cv & 3, u = slot & 15;
+      float f[8];
+      load_eight<E, ROPE>(A, static_cast<const T*>(A.k.p) + t * A.k.ts + h * A.k.hs, 8 * cv, cs + tl * half, f);
+      float most = magnitude(f, fine);
+      most = fmaxf(most, __uint_as_float(quad<0xb1>(__float_as_uint(most))));  // lanes 1 0 3 2
+      most = fmaxf(most, __uint_as_float(quad<0x4e>(__float_as_uint(most))));  // lanes 2 3 0 1
+      const int byte = scale_byte(most);
+      const float scale = __uint_as_float((uint32_t)byte << 23);
+      uint8_t* rec = record(C, slot, h);
+      *reinterpret_cast<uint32_t*>(rec + ((u * 4 + v) * nc + c) * 4) =
+          encode8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7], scale);
+      if (v == 0) rec[512 * nc + u * nc + c] = (uint8_t)byte;
+    }
+  }
+
+  // V: four lanes hold 4 consecutive tokens of one (head, group of 32): a word
+  // of codes spans them.  Where the tokens fill four neighbouring places of a
+  // unit the lanes trade bytes and write whole words; else each token writes
+  // its bytes.
   const int per_head = kCacheTokens * nc, at_once = kThreads / per_head;
   const int hl = threadIdx.x / per_head, r = threadIdx.x - hl * per_head;
   const int j = r & 3, c = (r >> 2) % nc, tl = (r >> 2) / nc * 4 + j, t = t0 + tl;
-  const int h_end = min((g + 1) * A.kv_heads_per_group, C.heads);
-  int slot = -1;
-  if (hl < at_once && tl < nt) {
-    slot = A.slots[t];
-    if ((unsigned)(slot >> C.bt_log2) >= (unsigned)C.blocks) slot = -1;
-    if (ROPE && A.pos[t] < 0) slot = -1;
-  }
-  // a quad whose tokens fill four neighbouring places of a unit writes V as
-  // whole words; else each token writes its bytes
-  const int s0 = (int)quad<0>((uint32_t)slot);
+  const int slot = hl < at_once ? s_slot[tl] : -1;
+  const int s0 = (int)quad_lane<0>((uint32_t)slot);
   const uint64_t in_row = __ballot(slot >= 0 && (s0 & 3) == 0 && slot == s0 + j);
   const bool whole = ((in_row >> (threadIdx.x & 60)) & 15) == 15;
-  bool fine = true;
-  for (int h = g * A.kv_heads_per_group + hl; h - hl < h_end; h += at_once) {
-    const bool live = slot >= 0 && hl < at_once && h < h_end;
+  for (int h = h_first + hl; h - hl < h_end; h += at_once) {
+    const bool live = slot >= 0 && h < h_end;
     uint8_t* rec = live ? record(C, slot, h) : nullptr;
     const int u = slot & 15;
     uint32_t q[4] = {0, 0, 0, 0};
     if (live) {
-      typedef typename E::T T;
       float f[32];
-      int byte;
-      load_group<E, ROPE>(A, static_cast<const T*>(A.k.p) + t * A.k.ts + h * A.k.hs, c, cs + tl * half, f);
-      fine &= scale_byte(f, byte);
-      float scale = __uint_as_float((uint32_t)byte << 23);
-#pragma unroll
-      for (int gg = 0; gg < 4; ++gg)
-        *reinterpret_cast<uint32_t*>(rec + ((u * 4 + gg) * nc + c) * 4) =
-            encode8(f[8 * gg], f[8 * gg + 1], f[8 * gg + 2], f[8 * gg + 3], f[8 * gg + 4], f[8 * gg + 5],
-                    f[8 * gg + 6], f[8 * gg + 7], scale);
-      rec[512 * nc + u * nc + c] = (uint8_t)byte;
       load_n<32>(static_cast<const T*>(A.v.p) + t * A.v.ts + h * A.v.hs + 32 * c, f);
-      fine &= scale_byte(f, byte);
-      scale = __uint_as_float((uint32_t)byte << 23);
+      const int byte = scale_byte(magnitude(f, fine));
+      const float scale = __uint_as_float((uint32_t)byte << 23);
       rec[528 * nc + u * nc + c] = (uint8_t)byte;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -272,7 +344,7 @@ __device__ __forceinline__ void cache_role(const RopeArgs& A, int block, double2
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t a0 = quad<0>(q[i]), a1 = quad<1>(q[i]), a2 = quad<2>(q[i]), a3 = quad<3>(q[i]);
+      const uint32_t a0 = quad_lane<0>(q[i]), a1 = quad_lane<1>(q[i]), a2 = quad_lane<2>(q[i]), a3 = quad_lane<3>(q[i]);
       if (i == j) w[0] = a0, w[1] = a1, w[2] = a2, w[3] = a3;
     }
     if (live) {
@@ -294,13 +366,14 @@ __device__ __forceinline__ void cache_role(const RopeArgs& A, int block, double2
 }
 
 template <class E, bool ROPE>
-__global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs A) {
+__global__ __launch_bounds__(kThreads, 4) void rope_kernel(const RopeArgs A) {
   // rotation role: 4 tokens in both precisions; cache role: 16 in fp64
   __shared__ double2 lds[ROPE ? kCacheTokens * kMaxPairs : 1];
+  __shared__ int s_slot[kCacheTokens];
   if ((int)blockIdx.x < A.rot_blocks) {
     if constexpr (ROPE) rotate_role<E>(A, blockIdx.x, lds);
   } else {
-    cache_role<E, ROPE>(A, blockIdx.x - A.rot_blocks, lds);
+    cache_role<E, ROPE>(A, blockIdx.x - A.rot_blocks, lds, s_slot);
   }
 }
 
