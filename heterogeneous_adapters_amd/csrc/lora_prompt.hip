@@ -205,7 +205,8 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
             (lds_s16x4*)(sv + v_at[d % kVVar] + 8 * e * (2 * D) + (d / kVVar) * (kVVar * 64)));
       vf[d] = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    if (key0 + kKeys - 1 > row_first) {
+    const bool masked = key0 + kKeys - 1 > row_first;
+    if (masked) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -232,19 +233,21 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
       pf[i >> 3][i & 7] = (__bf16)p;
     }
     // O^T += V^T P^T
+    auto v_frag = [&](int c, int d) {
+      s16x4 part[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {  // 16 tokens each
+      for (int e = 0; e < 2; ++e)
+        part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(sv + v_at[d % kVVar] + (16 * c + 8 * e) * (2 * D) + (d / kVVar) * (kVVar * 64)));
+      return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+#pragma unroll
+    for (int c = 0; c < 4; ++c)  // 16 tokens each
 #pragma unroll
       for (int d = 0; d < kDims; ++d) {
-        s16x4 part[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4*)(sv + v_at[d % kVVar] + (16 * c + 8 * e) * (2 * D) + (d / kVVar) * (kVVar * 64)));
-        const s16x8 a = c == 0 ? vf[d] : __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const s16x8 a = c == 0 ? vf[d] : v_frag(c, d);
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), pf[c], o[d], 0, 0, 0);
       }
-    }
   };
 
   // Two tiles per turn, one per buffer.  Every wave waits for its own copies
@@ -263,9 +266,10 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
     if ((it + 1) * kKeys <= row_last) compute((it + 1) * kKeys, s_k1, s_v1);
   }
 
-  l += __shfl_xor(l, 32);
-  if (row <= row_last) {
-    const float inv = 1.0f / l;
+  // A weight of zero does not hide an infinity or NaN of V from the product:
+  // rows that are not finite are computed again, key by key visible or not.
+  float odd = 0.0f;  // stays 0 while all is finite
+  auto write = [&](float inv, bool check) {
     uint16_t* out = static_cast<uint16_t*>(A.o.p) + (int64_t)(sp.begin + row) * A.o.ts + hq * A.o.hs;
 #pragma unroll
     for (int d = 0; d < kDims; ++d)
@@ -274,9 +278,98 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
         uint2 w;
         w.x = pack_bf2(o[d][i] * inv, o[d][i + 1] * inv);
         w.y = pack_bf2(o[d][i + 2] * inv, o[d][i + 3] * inv);
+        if (check) {
+          odd = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w.x), bf16x2{0, 0}, odd, false);
+          odd = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w.y), bf16x2{0, 0}, odd, false);
+        }
         *reinterpret_cast<uint2*>(out + 32 * d + 2 * i + 4 * h) = w;
       }
+  };
+  l += __shfl_xor(l, 32);
+  if (row <= row_last) write(1.0f / l, true);
+  if (!__any(odd != odd)) return;
+
+  // The long way, straight from global memory, 32 keys a step: the finite part
+  // of V as usual, then, for each sign and for NaN, a product that counts the
+  // visible ones.
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+    qf[s] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(A.q.p) +
+                                             (int64_t)(sp.begin + min(row, sp.len - 1)) * A.q.ts + hq * A.q.hs + 16 * s + 8 * h);
+#pragma unroll
+  for (int d = 0; d < kDims; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  m = kNone;
+  l = 0.0f;
+  for (int key0 = 0; key0 <= row_last; key0 += 32) {
+    f16v s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+    const uint16_t* kr = kbase + (int64_t)min(key0 + n, sp.len - 1) * A.k.ts + 8 * h;
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(kr + 16 * c), qf[c], s, 0, 0, 0);
+    float most = kNone;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (key0 + 8 * (i >> 2) + 4 * h + (i & 3) > row) s[i] = -INFINITY;
+      most = fmaxf(most, s[i] * A.scale_log2e);
+    }
+    most = fmaxf(most, __shfl_xor(most, 32));
+    const float mn = fmaxf(m, most), alpha = exp2_hw(m - mn);
+    m = mn;
+    l *= alpha;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) o[d] *= alpha;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      bf16x8 p, sees;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = exp2_hw(fmaf(s[8 * c + j], A.scale_log2e, -m));
+        l += x;
+        p[j] = (__bf16)x;
+        sees[j] = key0 + 16 * c + 8 * (j >> 2) + 4 * h + (j & 3) <= row ? (__bf16)1.0f : (__bf16)0.0f;
+      }
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) {
+        s16x8 a;
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = key0 + 16 * c + 8 * (j >> 2) + 4 * h + (j & 3);
+          a[j] = key < sp.len ? (short)vbase[(int64_t)key * A.v.ts + 32 * d + n] : (short)0;
+          bad = bad || (a[j] & 0x7f80) == 0x7f80;
+        }
+        if (__any(bad)) {
+          const s16x8 raw = a;
+#pragma unroll 1
+          for (int kind = 1; kind < 4; ++kind) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int bits = (uint16_t)raw[j], mag = bits & 0x7fff;
+              const int is = mag < 0x7f80 ? 0 : mag > 0x7f80 ? 3 : bits < 0x8000 ? 1 : 2;  // finite, +inf, -inf, NaN
+              a[j] = is == kind ? (short)0x3f80 : (short)0;
+            }
+            f16v count;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) count[i] = 0.0f;
+            count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), sees, count, 0, 0, 0);
+            const float add = kind == 1 ? INFINITY : kind == 2 ? -INFINITY : NAN;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (count[i] > 0.0f) o[d][i] += add;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[j] = (raw[j] & 0x7f80) == 0x7f80 ? (short)0 : raw[j];
+        }
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), p, o[d], 0, 0, 0);
+      }
+    }
   }
+  l += __shfl_xor(l, 32);
+  if (row <= row_last) write(1.0f / l, false);
 #endif
 }
 
@@ -337,9 +430,26 @@ __global__ __launch_bounds__(256) void prompt_f32_kernel(const PromptArgs A) {
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float* vr = vb + (int64_t)min(key0 + 4 * g + e, sp.len - 1) * A.v.ts + n;
+      const int key = key0 + 4 * g + e;
+      const float* vr = vb + (int64_t)min(key, sp.len - 1) * A.v.ts + n;
 #pragma unroll
-      for (int d = 0; d < kVecs; ++d) o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(vr[16 * d], p[e], o[d], 0, 0, 0);
+      for (int d = 0; d < kVecs; ++d) {
+        float v = key < sp.len ? vr[16 * d] : 0.0f;
+        const bool odd = !(fabsf(v) <= 3.402823466e38f);
+        if (masked && __any(odd)) {  // a weight of zero does not hide these: counted where they are seen
+          const float sees = key <= row ? 1.0f : 0.0f;
+          const float adds[3] = {INFINITY, -INFINITY, NAN};
+          const bool is[3] = {v > 3.402823466e38f, v < -3.402823466e38f, v != v};
+          for (int kind = 0; kind < 3; ++kind) {
+            const f4 count = __builtin_amdgcn_mfma_f32_16x16x4f32(is[kind] ? 1.0f : 0.0f, sees, f4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (count[i] > 0.0f) o[d][i] += adds[kind];
+          }
+          if (odd) v = 0.0f;
+        }
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, p[e], o[d], 0, 0, 0);
+      }
     }
   }
   l += __shfl_xor(l, 16);

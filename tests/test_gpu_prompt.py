@@ -59,3 +59,32 @@ def test_prompt_peaked_scores(dtype):
     q, v = normal(rng, (T, 2, 64), dtype), normal(rng, (T, 1, 64), dtype)
     k = R.round_to(normal(rng, (T, 1, 64), dtype) * np.linspace(0.1, 8.0, T)[:, None, None], dtype)
     check_prompt(run_prompt(q, k, v, [0, T], 0.9, dtype), q, k, v, [0, T], 0.9, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 96])
+def test_prompt_values_that_are_not_finite_stay_with_the_rows_that_see_them(dtype, D):
+    """NaN and infinities in V (and NaN in K) behind a row's last key, of its own prompt or the next one, change nothing."""
+    rng = np.random.default_rng(D)
+    lens = [150, 77]
+    indptr = np.concatenate([[0], np.cumsum(lens)])
+    T = int(indptr[-1])
+    q, k, v = normal(rng, (T, 2, D), dtype), normal(rng, (T, 1, D), dtype), normal(rng, (T, 1, D), dtype)
+    v[70, 0, 3], v[75, 0, 5], v[90, 0, 5], v[100, 0, 7] = np.nan, np.inf, -np.inf, np.inf
+    v[150, 0, :] = np.nan  # the second prompt's first token: all of its rows
+    k[120] = np.nan  # rows from 120 on of the first prompt are NaN
+    scale = 1.0 / math.sqrt(D)
+    got = run_prompt(q, k, v, indptr, scale, dtype)
+    clean_v, clean_k = np.where(np.isfinite(v), v, 0.0), np.where(np.isfinite(k), k, 0.0)
+    o, w, s_abs = R.attend_rows(q[:150], clean_k[:150], clean_v[:150], np.arange(1, 151), scale)
+    bound = R.attend_bound(o, w, s_abs, 150, D, dtype)
+    want = o.copy()
+    want[70:, :, 3] = np.nan
+    want[75:, :, 5] = np.inf
+    want[90:, :, 5] = np.nan
+    want[100:, :, 7] = np.inf
+    want[120:] = np.nan
+    fine = np.isfinite(want)
+    assert np.array_equal(np.isnan(got[:150]), np.isnan(want)) and np.array_equal(np.isposinf(got[:150]), np.isposinf(want))
+    assert np.all(np.abs(got[:150] - want)[fine] <= bound[fine])
+    assert np.isnan(got[150:]).all()
