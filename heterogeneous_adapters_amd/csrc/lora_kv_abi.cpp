@@ -392,6 +392,8 @@ lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, c
     if (lora_status_t st = check_heads(x, T, head_dim, dtype)) return st;
   if (q->heads != o->heads || k->heads != v->heads || q->heads % k->heads) return LORA_ERR_INVALID_ARG;
   if (T > 0 && (o->data == q->data || o->data == k->data || o->data == v->data)) return LORA_ERR_INVALID_ARG;
+  // a tile of 64 rows is addressed with 32-bit byte offsets
+  if (k->token_stride > (1 << 23) || v->token_stride > (1 << 23)) return LORA_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return LORA_OK;
   if (((int64_t)T / 64 + B) * q->heads >= kMaxBlocks) return LORA_ERR_UNSUPPORTED;
   PromptArgs A;

@@ -245,7 +245,9 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
  * token rows, prompt i in rows indptr[i] .. indptr[i+1]-1 (device, B+1
  * entries, ascending from 0 or later; entries are cut to [0, T]); row j of a
  * prompt attends to its rows 0..j.  Rows outside every prompt are not
- * written.  o may not overlap q, k or v.
+ * written.  Nothing behind a row's own place, infinities and NaN included,
+ * changes it.  o may not overlap q, k or v.  Token strides of k and v up to
+ * 2^23 elements; (T/64 + B) * heads < 2^23.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
 lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, const lora_heads_t* v,
                                  const lora_heads_t* o, const int32_t* indptr, int32_t B, int32_t T, int32_t head_dim,

@@ -1,0 +1,307 @@
+"""The attention operators together, as a serving step runs them: adapters on
+q/k/v, batch build, rotation and append, attention over cache and prompts; in
+captured graphs, on other streams, in one pool with the adapters, and at the
+edges of their contracts."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+import workloads as W
+from heterogeneous_adapters_amd import batch as dbatch
+from heterogeneous_adapters_amd import kv, lora
+from test_gpu_kv import DEV, Step, host, i32, make_table, normal, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def test_adapters_rope_cache_and_attention_in_one_pool():
+    """Two prefill prompts, then three decode steps over them, adapters and cache blocks in one page pool."""
+    hq, hkv, D, bt, PW, steps = 4, 2, 64, 64, 512, 3
+    lens = [90, 37]
+    T0, N = sum(lens), 3
+    projs = (("q", 256, hq * D), ("k", 256, hkv * D), ("v", 256, hkv * D))
+    w = W.make_workload(2, dict(T=T0, N=N, projs=projs, page_width=PW), keep_dense=False)
+    need = [-(-(n + steps) // bt) for n in lens]
+    n_adapter = w.pool.shape[0]
+    pages = n_adapter + sum(need) + 2
+    base = torch.zeros((pages, 16 * PW), dtype=torch.bfloat16, device=DEV)
+    base[:n_adapter] = dbatch.host_to_device(w.pool.reshape(n_adapter, -1), "bf16", DEV)
+    b = dbatch.to_device(w, device=DEV, pool=base)
+    alloc = lora.PageCache(pages)
+    alloc.admit(0, n_adapter)  # the adapters' pages
+    free = np.concatenate([alloc.admit(1 + i, n)[1] for i, n in enumerate(need)])
+    assert free.min() >= n_adapter
+    cache = kv.Cache.in_pool(lora.Pool(base, PW), bt, hkv, D)
+    before = base[:n_adapter].view(torch.int16).clone()
+    table = torch.full((2, max(need) + 1), -1, dtype=torch.int32, device=DEV)
+    bat = kv.Batch(T0, 4, hq, hkv, D)
+    ws = kv.attend_workspace(bat)
+    rope = kv.Rope.scaled(D, scaling=kv.SCALING_LINEAR, factor=2.0, device=DEV)
+    freq, scale = R.frequencies(D, 1e4, "linear", 2.0, 0)
+    sm = 1.0 / math.sqrt(D)
+    segs = lora.Segments(T0, N)
+    lws = lora.workspace(T0, N, 3, 256)
+    ctx, new, used = np.array([0, 0]), np.array(lens), 0
+    past = [[], []]  # per request, cached (k, v) rows as values
+    for step in range(1 + steps):
+        T = int(new.sum())
+        lora.lora_apply(b.ids[:T].contiguous(), segs, T, b.projs, b.adapters, b.pool, lws)
+        q, k, v = (b.Y[i][:T].unflatten(1, (-1, D)) for i in range(3))
+        kv.lora_kv_build(i32(ctx), i32(new), T, table, i32(free[used:]), cache.num_blocks, bt, bat)
+        qr, kr, out, pout = (torch.zeros_like(x) for x in (q, k, q, q))
+        kv.lora_kv_append(q, qr, k, v, bat.positions, bat.slots, rope, cache, bat)
+        kv.lora_kv_attend(qr, out, bat, table, cache, sm, ws)
+        kv.lora_rope(None, None, k, kr, bat.positions, rope)
+        if step == 0:  # whole prompts: exact K and V in place of the cached ones
+            kv.lora_prompt_attend(qr, kr, v, pout, bat.q_indptr, sm)
+        torch.cuda.synchronize()
+        assert int(bat.flags) == 0
+        used += int(bat.new_blocks)
+        row = 0
+        for i in range(2):
+            n = int(new[i])
+            qi, ki, vi = (host(x[row:row + n]) for x in (qr, kr, v))
+            want_q = R.rotate(host(q[row:row + n]), ctx[i] + np.arange(n), freq, scale, False)
+            assert np.all(np.abs(qi - want_q) <= 2.0 ** -8 * np.abs(want_q) + 1e-6 * np.abs(want_q).max())
+            if step == 0:
+                o, a, s = R.attend_rows(qi, ki, vi, np.arange(1, n + 1), sm)
+                assert np.all(np.abs(host(pout[row:row + n]) - o) <= R.attend_bound(o, a, s, n, D, "bf16"))
+            quant = lambda x: R.values(*R.quantise(x.reshape(n, hkv, -1, 32))).reshape(n, hkv, D)  # noqa: E731
+            past[i].append((quant(ki), quant(vi)))
+            K, V = (np.concatenate([p[j] for p in past[i]]) for j in (0, 1))
+            o, a, s = R.attend_rows(qi, K, V, ctx[i] + np.arange(n) + 1, sm)
+            assert np.all(np.abs(host(out[row:row + n]) - o) <= R.attend_bound(o, a, s, len(K), D, "bf16")), (step, i)
+            row += n
+        ctx, new = ctx + new, np.array([1, 1])
+    assert torch.equal(base[:n_adapter].view(torch.int16), before) and used == sum(need)
+
+
+def test_captured_decode_steps_replay_as_lengths_grow():
+    """build, append and attend captured once; lengths move on the device between replays."""
+    hq, hkv, D, bt, B = 8, 2, 64, 16, 5
+    rng = np.random.default_rng(4)
+    ctx0 = np.array([0, 14, 15, 1030, 3000])
+    width = -(-int(ctx0.max() + 40) // bt)
+    num = B * width
+    ids = rng.permutation(num).reshape(B, width)
+    table0 = np.full((B, width), -1)
+    for i in range(B):
+        h = -(-int(ctx0[i]) // bt)
+        table0[i, :h] = ids[i, :h]
+    free0 = np.concatenate([ids[i, -(-int(ctx0[i]) // bt):] for i in range(B)])
+    data0 = rng.integers(0, 256, (num, R.block_bytes(bt, hkv, D))).astype(np.uint8)
+    nc = D // 32
+    recs = data0.reshape(num, hkv, bt // 16, 544 * nc)
+    recs[..., 512 * nc:] = 120 + recs[..., 512 * nc:] % 8
+    rope = kv.Rope.scaled(D, device=DEV)
+    ctx, new, free = i32(ctx0), torch.ones(B, dtype=torch.int32, device=DEV), i32(free0)
+    q, k, v = (torch.empty((B, h, D), dtype=torch.bfloat16, device=DEV) for h in (hq, hkv, hkv))
+
+    class Side:
+        def __init__(self):
+            self.table, self.data = i32(table0), torch.tensor(data0, device=DEV)
+            self.cache = kv.Cache(self.data, bt, hkv, D)
+            self.bat = kv.Batch(B, B, hq, hkv, D)
+            self.ws, self.qr, self.out = kv.attend_workspace(self.bat), torch.empty_like(q), torch.empty_like(q)
+
+        def step(self):
+            kv.lora_kv_build(ctx, new, B, self.table, free, num, bt, self.bat)
+            kv.lora_kv_append(q, self.qr, k, v, self.bat.positions, self.bat.slots, rope, self.cache, self.bat)
+            kv.lora_kv_attend(self.qr, self.out, self.bat, self.table, self.cache, 0.125, self.ws)
+
+    graphed, eager = Side(), Side()
+    for x in (q, k, v):
+        x.normal_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graphed.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed.step()
+    eager.step()
+    for it in range(6):
+        for x in (q, k, v):
+            x.normal_()
+        graph.replay()
+        eager.step()
+        torch.cuda.synchronize()
+        assert torch.equal(graphed.out, eager.out) and torch.equal(graphed.table, eager.table), it
+        assert torch.equal(graphed.data, eager.data)
+        # the caller's bookkeeping: blocks of the front of the free list are gone
+        taken = int(eager.bat.new_blocks)
+        free.copy_(torch.roll(free, -taken))
+        ctx.add_(1)
+    assert int(eager.bat.flags) == 0
+
+
+def test_side_streams_with_buffers_of_their_own():
+    steps = [Step(20 + i, np.array([700, 33, 5]), np.array([1, 4, 1]), 8, 2, 64, 16, "bf16") for i in range(2)]
+    alone = [s.run(0.125) for s in steps]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, st in zip(steps, streams):
+            kv.lora_kv_build(i32(s.ctx), i32(s.new), s.T, s.tab, i32(s.free), s.num, s.bt, s.batch, stream=None)
+        torch.cuda.synchronize()
+        for s, st in zip(steps, streams):
+            s.out.zero_()
+        torch.cuda.synchronize()
+        for s, st in zip(steps, streams):
+            kv.lora_kv_attend(s.dq, s.out, s.batch, s.tab, s.cache, 0.125, s.ws, stream=st)
+        torch.cuda.synchronize()
+        for s, want in zip(steps, alone):
+            assert np.array_equal(host(s.out), want)
+
+
+def test_a_split_request_gives_the_same_bits_every_time():
+    s = Step(31, np.array([9000]), np.array([1]), 8, 1, 64, 64, "bf16")
+    want = s.run(0.125)
+    assert int(s.batch.counts[kv.COUNT_PARTS]) > 1
+    s.check(want, 0.125)
+    for _ in range(30):
+        s.out.fill_(5.0)
+        kv.lora_kv_attend(s.dq, s.out, s.batch, s.tab, s.cache, 0.125, s.ws)
+        torch.cuda.synchronize()
+        assert np.array_equal(host(s.out), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ctx,new,hq,hkv,D", [([2500, 0, 1100], [37, 20, 1], 8, 2, 64), ([3000], [9], 12, 2, 128), ([2100], [40], 2, 2, 256),
+                                              ([1500, 2], [70, 1], 16, 1, 32)])
+def test_split_requests_with_many_new_tokens(ctx, new, hq, hkv, D, dtype):
+    s = Step(40 + D, np.array(ctx), np.array(new), hq, hkv, D, 16, dtype, pad=2)
+    got = s.run(1.0 / math.sqrt(D))
+    assert int(s.batch.counts[kv.COUNT_PARTS]) > 1 and int(s.batch.counts[kv.COUNT_WIDE]) > 0
+    s.check(got, 1.0 / math.sqrt(D))
+
+
+def test_blocks_outside_the_cache_are_not_attended():
+    s = Step(50, np.array([100, 60]), np.array([1, 1]), 4, 2, 64, 16, "bf16")
+    s.run(0.125)
+    bad = s.tab.clone()
+    bad[0, 2], bad[0, 5], bad[1, 0:4] = s.num + 3, -4, 1 << 30
+    out = torch.full_like(s.dq, 5.0)
+    kv.lora_kv_attend(s.dq, out, s.batch, bad, s.cache, 0.125, s.ws)
+    torch.cuda.synchronize()
+    assert int(s.batch.flags) == kv.FLAG_BLOCK_RANGE
+    keep = np.array([p // 16 not in (2, 5) for p in range(101)])
+    o, a, sa = R.attend_rows(s.q[:1], s.k[:101][keep], s.v[:101][keep], [int(keep.sum())], 0.125)
+    assert np.all(np.abs(host(out)[:1] - o) <= R.attend_bound(o, a, sa, 101, 64, "bf16"))
+    assert bool((out[1] == 0).all())  # a row that sees no token
+
+
+def test_a_batch_that_was_not_built_for_the_call_writes_nothing():
+    s = Step(51, np.array([10, 20]), np.array([1, 1]), 4, 2, 64, 16, "bf16")
+    s.run(0.125)
+    fresh = kv.Batch(s.T + 3, 4, 4, 2, 64)
+    fresh._resize(s.T, 2)
+    other = kv.Batch(s.T + 3, 4, 4, 2, 64)
+    kv.lora_kv_build(i32([1, 2, 3]), i32([1, 1, 1]), 3, i32(np.zeros((3, 2))), i32([]), 4, 16, other)
+    other._resize(s.T, 2)
+    for b in (fresh, other):
+        out = torch.full_like(s.dq, 5.0)
+        kv.lora_kv_attend(s.dq, out, b, s.tab, s.cache, 0.125, s.ws)
+        torch.cuda.synchronize()
+        assert bool((out == 5.0).all()) and int(b.flags) == kv.FLAG_BATCH
+
+
+def test_free_list_that_ran_out_leaves_the_rest_uncached():
+    """Tokens without a block: slot -1, not appended, not attended; the others as ever."""
+    hq, hkv, D, bt = 2, 1, 64, 16
+    rng = np.random.default_rng(8)
+    new = np.array([20, 30])
+    data = torch.zeros((3, R.block_bytes(bt, hkv, D)), dtype=torch.uint8, device=DEV)
+    cache, bat = kv.Cache(data, bt, hkv, D), kv.Batch(50, 2, hq, hkv, D)
+    table = i32(np.full((2, 4), -1))
+    kv.lora_kv_build(i32([0, 0]), i32(new), 50, table, i32([2, 0, 1]), 3, bt, bat)
+    q, k, v = (normal(rng, (50, h, D), "bf16") for h in (hq, hkv, hkv))
+    kv.lora_kv_append(None, None, to_dev(k, "bf16"), to_dev(v, "bf16"), None, bat.slots, None, cache)
+    out = torch.full((50, hq, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    kv.lora_kv_attend(to_dev(q, "bf16"), out, bat, table, cache, 0.125, kv.attend_workspace(bat))
+    torch.cuda.synchronize()
+    assert int(bat.flags) == kv.FLAG_FREE_LIST and bat.kv_len.tolist() == [20, 16]
+    quant = lambda x: R.values(*R.quantise(x.reshape(-1, hkv, 2, 32))).reshape(-1, hkv, D)  # noqa: E731
+    K, V = quant(k[20:36]), quant(v[20:36])
+    sees = np.minimum(np.arange(1, 31), 16)
+    o, a, s = R.attend_rows(q[20:], K, V, sees, 0.125)
+    assert np.all(np.abs(host(out)[20:] - o) <= R.attend_bound(o, a, s, 16, D, "bf16"))
+
+
+def test_offsets_past_32_bits():
+    """Blocks and rows more than 4 GB apart."""
+    hq, hkv, D, bt = 2, 1, 64, 16
+    rng = np.random.default_rng(12)
+    far = 1 << 30
+    data = torch.zeros((6, far), dtype=torch.uint8, device=DEV)  # 6 GB, one block per GB
+    cache = kv.Cache(data, bt, hkv, D)
+    T = 5
+    stride = 700_000_000  # elements between rows: 1.4 GB
+    big = torch.zeros(3 * T * 64 + (T - 1) * stride + 4096, dtype=torch.bfloat16, device=DEV)
+    view = lambda off, h: torch.as_strided(big, (T, h, D), (stride, D, 1), off)  # noqa: E731
+    q, k, v, qo, out = view(0, hq), view(256, hkv), view(512, hkv), view(768, hq), view(1024, hq)
+    qv, kv_, vv = (normal(rng, (T, h, D), "bf16") for h in (hq, hkv, hkv))
+    q.copy_(to_dev(qv, "bf16")), k.copy_(to_dev(kv_, "bf16")), v.copy_(to_dev(vv, "bf16"))
+    bat = kv.Batch(T, 1, hq, hkv, D)
+    table = i32([[5, 4]])
+    kv.lora_kv_build(i32([0]), i32([T]), T, i32(np.full((1, 2), -1)), i32([5, 4]), 6, bt, bat)
+    rope = kv.Rope.scaled(D, device=DEV)
+    kv.lora_kv_append(q, qo, k, v, bat.positions, bat.slots, rope, cache)
+    kv.lora_kv_attend(qo, out, bat, table, cache, 0.125, kv.attend_workspace(bat))
+    near, qn = torch.zeros((T, hkv, D), dtype=torch.bfloat16, device=DEV), torch.zeros((T, hq, D), dtype=torch.bfloat16, device=DEV)
+    kv.lora_rope(to_dev(qv, "bf16"), qn, to_dev(kv_, "bf16"), near, bat.positions, rope)
+    torch.cuda.synchronize()
+    assert torch.equal(qn, qo)
+    quant = lambda x: R.values(*R.quantise(x.reshape(-1, hkv, 2, 32))).reshape(-1, hkv, D)  # noqa: E731
+    K, V = quant(host(near)), quant(vv)
+    gk, gv = torch.zeros_like(near), torch.zeros_like(near)
+    kv.lora_kv_gather(cache, bat.slots, gk, gv)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(gk), K) and np.array_equal(host(gv), V)
+    o, a, s = R.attend_rows(host(qn), K, V, np.arange(1, T + 1), 0.125)
+    assert np.all(np.abs(host(out) - o) <= R.attend_bound(o, a, s, T, D, "bf16"))
+
+
+def test_prompt_rows_far_apart_and_heads_first():
+    """Row strides of a fused projection, heads-first tensors, and rows gigabytes apart."""
+    rng = np.random.default_rng(13)
+    T, hq, hkv, D = 150, 4, 2, 64
+    q, k, v = (normal(rng, (T, h, D), "bf16") for h in (hq, hkv, hkv))
+    fused = torch.full((T, hq + 2 * hkv + 3, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for at, x in ((0, q), (hq, k), (hq + hkv, v)):
+        fused[:, at:at + x.shape[1]] = to_dev(x, "bf16")
+    fq, fk, fv = fused[:, :hq], fused[:, hq:hq + hkv], fused[:, hq + hkv:hq + 2 * hkv]
+    plain = torch.zeros((T, hq, D), dtype=torch.bfloat16, device=DEV)
+    kv.lora_prompt_attend(to_dev(q, "bf16"), to_dev(k, "bf16"), to_dev(v, "bf16"), plain, i32([0, T]), 0.125)
+    out = torch.zeros_like(plain)
+    kv.lora_prompt_attend(fq, fk, fv, out, i32([0, T]), 0.125)
+    first = [to_dev(x, "bf16").transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]
+    out2 = torch.zeros((hq, T, D), dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    kv.lora_prompt_attend(*first, out2, i32([0, T]), 0.125)
+    wide = torch.zeros((T - 1) * 8_000_000 + 4096, dtype=torch.bfloat16, device=DEV)
+    far = [torch.as_strided(wide, x.shape, (8_000_000, D, 1), off) for off, x in ((0, q), (1024, k), (2048, v))]
+    for dst, x in zip(far, (q, k, v)):
+        dst.copy_(to_dev(x, "bf16"))
+    out3 = torch.zeros_like(plain)
+    kv.lora_prompt_attend(*far, out3, i32([0, T]), 0.125)
+    torch.cuda.synchronize()
+    assert torch.equal(plain, out) and torch.equal(plain, out2) and torch.equal(plain, out3)
+
+
+def test_prompt_offsets_that_do_not_ascend_stay_in_bounds():
+    q = torch.randn((100, 2, 64), device=DEV).bfloat16()
+    out = torch.full_like(q, 5.0)
+    for ptr in ([0, 500], [50, 20], [-9, 30, 10, 100], [99, 99, 100], [100, 100], [2 ** 31 - 1, -2 ** 31]):
+        kv.lora_prompt_attend(q, q, q, out, i32(ptr), 0.125)
+        kv.lora_prompt_attend(q.float(), q.float(), q.float(), out.float(), i32(ptr), 0.125)
+    torch.cuda.synchronize()
+    want = torch.full_like(q, 5.0)
+    out.fill_(5.0)
+    kv.lora_prompt_attend(q, q, q, out, i32([0, 500]), 0.125)
+    kv.lora_prompt_attend(q, q, q, want, i32([0, 100]), 0.125)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
