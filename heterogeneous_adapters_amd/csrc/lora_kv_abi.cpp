@@ -14,7 +14,8 @@ using namespace lora::kv;
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // work-groups of 512 threads: a launch has under 2^32 threads
+// A launch has under 2^32 threads: work-groups of 512, four for a work item.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23, kMaxItems = kMaxBlocks / 4;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -82,7 +83,8 @@ struct BatchSizes {
 bool batch_ok(int32_t max_tokens, int32_t max_seqs, int32_t hq, int32_t hkv, int32_t head_dim) {
   return max_tokens >= 0 && max_tokens <= LORA_MAX_TOKENS && max_seqs >= 1 && max_seqs <= LORA_KV_MAX_SEQS &&
          hkv >= 1 && hq >= hkv && hq <= LORA_KV_MAX_HEADS && hq % hkv == 0 && head_dim_ok(head_dim) &&
-         item_cap(max_tokens, max_seqs, hkv, hq / hkv) * hkv < kMaxBlocks;
+         (int64_t)max_tokens * (hq / hkv) < 0x7fffff00ll &&
+         item_cap(max_tokens, max_seqs, hkv, hq / hkv) * hkv < kMaxItems;
 }
 BatchSizes batch_sizes(int32_t max_tokens, int32_t max_seqs, int32_t hq, int32_t hkv) {
   BatchSizes z;
@@ -90,7 +92,7 @@ BatchSizes batch_sizes(int32_t max_tokens, int32_t max_seqs, int32_t hq, int32_t
   z.kv_len = align_up(4 * (size_t)max_seqs);
   z.row = align_up(4 * (size_t)std::max(max_tokens, 1));
   z.counts = align_up(4 * kNumCounts);
-  z.items = align_up(2 * 16 * (size_t)item_cap(max_tokens, max_seqs, hkv, hq / hkv));
+  z.items = align_up(kClasses * 32 * (size_t)item_cap(max_tokens, max_seqs, hkv, hq / hkv));
   z.arrive = align_up(4 * (size_t)part_cap(hkv) * hkv);
   z.total = z.q_indptr + z.kv_len + 3 * z.row + z.counts + z.items + z.arrive;
   return z;
@@ -360,9 +362,6 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
   AttendArgs A;
   A.q = rows_of(q);
   A.o = rows_of(o);
-  A.q_indptr = batch->q_indptr;
-  A.kv_len = batch->kv_len;
-  A.positions = batch->positions;
   A.counts = batch->counts;
   A.items = reinterpret_cast<const int4*>(batch->plan);
   A.arrive = batch->plan + z.items / 4;
@@ -373,12 +372,11 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
   A.B = B;
   A.G = batch->num_q_heads / batch->num_kv_heads;
   A.item_cap = (int32_t)item_cap(batch->max_tokens, batch->max_seqs, batch->num_kv_heads, A.G);
-  A.part_cap = (int32_t)part_cap(batch->num_kv_heads);
   A.cache = cache_of(cache);
   A.scale_log2e = scale * 1.4426950408889634f;
   A.part = static_cast<float*>(ws);
   const int64_t blocks = item_cap(T, B, batch->num_kv_heads, A.G) * batch->num_kv_heads;
-  return hip(launch_attend(A, dtype, (int)blocks, wide_step(T, B), static_cast<hipStream_t>(stream)));
+  return hip(launch_attend(A, dtype, (int)blocks, many_rows(T, B), static_cast<hipStream_t>(stream)));
 }
 
 lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, const lora_heads_t* v,

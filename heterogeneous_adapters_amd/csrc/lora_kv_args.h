@@ -55,13 +55,12 @@ struct RopeArgs {
 
 struct AttendArgs {
   Rows q, o;
-  const int32_t *q_indptr, *kv_len, *positions;
   int32_t* counts;
   const int4* items;
   int32_t* arrive;
   const int32_t* table;
   int64_t tstride;
-  int32_t width, T, B, G, item_cap, part_cap;
+  int32_t width, T, B, G, item_cap;
   Cache cache;
   float scale_log2e;
   float* part;
@@ -77,7 +76,7 @@ struct PromptArgs {
 hipError_t launch_build(const BuildArgs& A, hipStream_t s);
 hipError_t launch_rope(const RopeArgs& A, int dtype, int blocks, hipStream_t s);
 hipError_t launch_gather(const RopeArgs& A, int dtype, hipStream_t s);
-hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, bool wide, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, bool many, hipStream_t s);
 hipError_t launch_prompt(const PromptArgs& A, int dtype, int D, hipStream_t s);
 
 }  // namespace kv

@@ -91,42 +91,166 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&f)[NS]) {
 // Whether the batch's plan was built for this call.
 __device__ __forceinline__ bool plan_ok(const AttendArgs& A) {
   const int32_t* c = A.counts;
-  return c[kCountCheck] == check_word(c[kCountB], c[kCountT], c[kCountItems], c[kCountWide], c[kCountParts]) &&
-         c[kCountB] == A.B && c[kCountT] == A.T && c[kCountItems] <= A.item_cap && c[kCountWide] <= A.item_cap;
+  return c[kCountCheck] == check_word(c[kCountB], c[kCountT], c[kCountItems], c[kCountMid], c[kCountWide], c[kCountParts]) &&
+         c[kCountB] == A.B && c[kCountT] == A.T && c[kCountItems] <= A.item_cap && c[kCountMid] <= A.item_cap &&
+         c[kCountWide] <= A.item_cap;
+}
+
+// A work item: its request, rows and keys.
+struct Item {
+  int seq, row0, ci, part;    // part: the tile's first partial result, -1 when the tile is not split
+  int qs, nrows, pos0, kv;    // first token row, rows, first position, cached tokens
+  int begin, end, chunks;     // keys of this item, items of the tile
+};
+// The descriptor is read along with the counters it is checked against (the
+// grid stays within the list's capacity), so that one trip to memory serves
+// both.  `rows`: rows that the kernel takes of the tile, from row0 + skip on.
+__device__ __forceinline__ bool read_item(const AttendArgs& A, int cls, int count_at, int item, int skip, int rows, Item& it) {
+  const int4* d = A.items + 2 * ((int64_t)cls * A.item_cap + item);
+  const int4 x = d[0], y = d[1];
+  const int chunk = A.counts[kCountChunk];
+  if (!plan_ok(A)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
+    return false;
+  }
+  if (item >= A.counts[count_at]) return false;
+  it.seq = uniform(x.x), it.row0 = uniform(x.y) + skip, it.ci = uniform(x.z), it.part = uniform(x.w);
+  it.qs = uniform(y.x), it.nrows = uniform(y.y), it.pos0 = uniform(y.z), it.kv = uniform(y.w);
+  if (it.row0 >= it.nrows) return false;
+  const int sees = min(it.pos0 + min(it.row0 + rows - 1, it.nrows - 1) / A.G + 1, it.kv);
+  it.begin = it.part < 0 ? 0 : it.ci * chunk;
+  it.end = it.part < 0 ? sees : min(it.begin + chunk, sees);
+  it.chunks = it.part < 0 ? 1 : (it.kv + chunk - 1) / chunk;
+  return true;
 }
 
 // Reciprocal of a row's sum: zero for a row that saw no key, NaN kept.
 __device__ __forceinline__ float inverse(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l); }
 
-// RT: tiles of 16 rows per work item (1, or 2 for requests of many rows).
-// W: waves per work-group.
-template <class E, int NC, int RT, int W>
+// A part (16 rows of one chunk): rows of D sums, then (m, l) pairs.  A tile's
+// parts lie by chunk, then by 16 rows.
+template <int D>
+__device__ __forceinline__ float* part_at(const AttendArgs& A, int part, int kvh) {
+  return A.part + ((int64_t)part * A.cache.heads + kvh) * (kUnit * (D + 2));
+}
+
+// Four dims of an output row.
+template <class E>
+__device__ __forceinline__ void store_out(const AttendArgs& A, const Item& it, int kvh, int row, int d, f4 acc, float inv) {
+  typedef typename E::T T;
+  const int jr = row / A.G;
+  T* out = static_cast<T*>(A.o.p) + (int64_t)(it.qs + jr) * A.o.ts + (kvh * A.G + row - jr * A.G) * A.o.hs + d;
+  if constexpr (sizeof(T) == 2) {
+    uint2 w;
+    w.x = pack_bf2(acc[0] * inv, acc[1] * inv);
+    w.y = pack_bf2(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2*>(out) = w;
+  } else {
+    *reinterpret_cast<f4*>(out) = acc * inv;
+  }
+}
+
+// Counts a work-group's arrival at its tile; true in the one that comes last,
+// for which every part of the tile is visible.  A wave's wait makes its own
+// stores visible before the arrival is counted.
+__device__ __forceinline__ bool arrive_last(const AttendArgs& A, const Item& it, int part, int kvh, int* s_last) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  wait_vm<0>();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int32_t* count = A.arrive + (int64_t)part * A.cache.heads + kvh;
+    const int before = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *s_last = before == it.chunks - 1;
+    if (*s_last) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next layer
+  }
+  __syncthreads();
+  const bool last = *s_last != 0;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+  return last;
+}
+
+// Joins the chunks of `rt` times 16 rows from it.row0 on, whose first parts
+// are `part`, part + 1, ..; `units` parts per chunk.  In the order of the
+// chunks, whichever work-group does it.  scratch: 6 floats per thread.
+template <class E, int D, int kThreads>
+__device__ __forceinline__ void join(const AttendArgs& A, const Item& it, int part, int units, int rt, int kvh, float* scratch) {
+  constexpr int kVecs = D / 4;
+  for (int r = 0; r < rt; ++r) {
+    const int live = min(it.nrows - it.row0 - r * kUnit, kUnit);
+    if (live <= 0) break;
+    const int tasks = live * kVecs;
+    const int groups = max(1, min(kThreads / tasks, it.chunks));  // threads per task, each every groups-th chunk
+    for (int t0 = 0; t0 < tasks; t0 += kThreads) {  // more than one turn only with one group
+      const int grp = threadIdx.x / tasks, task = t0 + threadIdx.x - (groups > 1 ? grp * tasks : 0);
+      const int row = task / kVecs, d = (task - row * kVecs) * 4;
+      const bool work = task < tasks && (groups == 1 || grp < groups);
+      float M = kNone, L = 0.0f;
+      f4 acc{0, 0, 0, 0};
+      if (work) {
+        for (int c = groups > 1 ? grp : 0; c < it.chunks; c += 4 * groups) {
+          float2 ml[4], lo[4], hi[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float* p = part_at<D>(A, part + min(c + e * groups, it.chunks - 1) * units + r, kvh);
+            ml[e] = get2(p + kUnit * D + 2 * row);
+            lo[e] = get2(p + row * D + d);
+            hi[e] = get2(p + row * D + d + 2);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (c + e * groups >= it.chunks) break;
+            const float mn = fmaxf(M, ml[e].x), a = exp2_hw(M - mn), b = exp2_hw(ml[e].x - mn);
+            M = mn;
+            L = L * a + ml[e].y * b;
+            acc = acc * a + b * f4{lo[e].x, lo[e].y, hi[e].x, hi[e].y};
+          }
+        }
+      }
+      if (groups > 1) {
+        __syncthreads();
+        if (work) {
+          float* s = scratch + threadIdx.x * 6;
+          s[0] = M, s[1] = L;
+          s[2] = acc[0], s[3] = acc[1], s[4] = acc[2], s[5] = acc[3];
+        }
+        __syncthreads();
+        if (work && grp == 0) {
+          for (int e = 1; e < groups; ++e) {
+            const float* s = scratch + (threadIdx.x + e * tasks) * 6;
+            const float mn = fmaxf(M, s[0]), a = exp2_hw(M - mn), b = exp2_hw(s[0] - mn);
+            M = mn;
+            L = L * a + s[1] * b;
+            acc = acc * a + b * f4{s[2], s[3], s[4], s[5]};
+          }
+        }
+      }
+      if (work && grp == 0) store_out<E>(A, it, kvh, it.row0 + r * kUnit + row, d, acc, inverse(L));
+      if (groups > 1) break;
+    }
+  }
+}
+
+// RT: tiles of 16 rows per work item.  CLS: the items' class; the fp32 kernel
+// takes the 128 rows of class 2 in four pieces.  W: waves per work-group.
+template <class E, int NC, int RT, int CLS, int W>
 __global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T) == 2 ? 4 : 1) void attend_kernel(const AttendArgs A) {
   constexpr int kThreads = 64 * W;
   constexpr int NS = sizeof(typename E::T) == 2 ? 1 : 3;
   constexpr int D = 32 * NC, LD = D + 4, kVecs = D / 4;
+  constexpr int kPieces = CLS == 2 ? kWideRows / (kUnit * RT) : 1, kUnits = RT * kPieces;
   typedef typename E::T T;
   __shared__ float s_o[W][kUnit][LD];
   __shared__ float s_m[W][kUnit], s_l[W][kUnit];
   __shared__ int s_last;
 
   const int hkv = A.cache.heads;
-  const int item = blockIdx.x / hkv, kvh = blockIdx.x - item * hkv;
-  if (!plan_ok(A)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
-    return;
-  }
-  if (item >= A.counts[RT == 1 ? kCountItems : kCountWide]) return;
-  const int chunk = A.counts[kCountChunk];
-  const int4 desc = A.items[RT == 1 ? item : A.item_cap + item];
-  const int seq = uniform(desc.x), tile = uniform(desc.y), ci = uniform(desc.z), part = uniform(desc.w);
-  const int qs = uniform(A.q_indptr[seq]), qe = uniform(A.q_indptr[seq + 1]), kv = uniform(A.kv_len[seq]);
-  const int G = A.G, nrows = (qe - qs) * G, row0 = tile * (kUnit * RT);
-  const int pos0 = uniform(A.positions[qs]);
+  const int item = blockIdx.x / (hkv * kPieces), piece = blockIdx.x / hkv % kPieces, kvh = blockIdx.x % hkv;
+  Item it;
+  if (!read_item(A, CLS, CLS == 0 ? kCountItems : CLS == 1 ? kCountMid : kCountWide, item, piece * RT * kUnit, RT * kUnit, it)) return;
+  const int part = it.part < 0 ? -1 : it.part + piece * RT;
+  const int G = A.G, nrows = it.nrows, row0 = it.row0, qs = it.qs, pos0 = it.pos0, kv = it.kv, begin = it.begin, end = it.end;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
   const int limit0 = uniform(min(pos0 + row0 / G + 1, kv));
-  const int begin = ci * chunk;
-  const int end = min(begin + chunk, uniform(min(pos0 + min(row0 + kUnit * RT - 1, nrows - 1) / G + 1, kv)));
 
   int limit[RT];  // this lane's rows see tokens below these
   bf16x8 qf[RT][NC][NS];
@@ -153,7 +277,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T)
     for (int c = 0; c < NC; ++c) o[r][c][0] = o[r][c][1] = f4{0, 0, 0, 0};
   }
 
-  const int32_t* trow = A.table + (int64_t)seq * A.tstride;
+  const int32_t* trow = A.table + (int64_t)it.seq * A.tstride;
   const uint8_t* head = A.cache.base + ((int64_t)kvh << A.cache.bt_log2 >> 4) * (544 * NC);
   const int unit_mask = (1 << (A.cache.bt_log2 - 4)) - 1;
   const int first = begin / kTile + wave, last = (end + kTile - 1) / kTile;  // steps first, first+W, .. < last
@@ -295,23 +419,6 @@ __global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T)
   }
   if (__any(bad_block) && lane == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BLOCK_RANGE);
 
-  // Output rows of tile r; a row's four dims from d.
-  auto store = [&](int r, int i, int d, f4 acc, float inv) {
-    const int row = row0 + r * kUnit + i, jr = row / G;
-    T* out = static_cast<T*>(A.o.p) + (int64_t)(qs + jr) * A.o.ts + (kvh * G + row - jr * G) * A.o.hs + d;
-    if constexpr (sizeof(T) == 2) {
-      uint2 w;
-      w.x = pack_bf2(acc[0] * inv, acc[1] * inv);
-      w.y = pack_bf2(acc[2] * inv, acc[3] * inv);
-      *reinterpret_cast<uint2*>(out) = w;
-    } else {
-      *reinterpret_cast<f4*>(out) = acc * inv;
-    }
-  };
-  // A part (16 rows of one chunk): rows of D sums, then (m, l) pairs.
-  constexpr int kPart = kUnit * (D + 2);
-  auto part_at = [&](int c, int r) { return A.part + ((int64_t)(part + c * RT + r) * hkv + kvh) * kPart; };
-
   // join the waves
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -344,117 +451,264 @@ __global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T)
         acc += a * *reinterpret_cast<const f4*>(&s_o[w][row][d]);
       }
       if (part < 0) {
-        store(r, row, d, acc, inverse(L));
+        store_out<E>(A, it, kvh, row0 + r * kUnit + row, d, acc, inverse(L));
       } else {
-        float* p = part_at(ci, r);
+        float* p = part_at<D>(A, part + it.ci * kUnits + r, kvh);
         put2(p + row * D + d, acc[0], acc[1]);
         put2(p + row * D + d + 2, acc[2], acc[3]);
         if (d == 0) put2(p + kUnit * D + 2 * row, M, L);
       }
     }
   }
-  if (part < 0) return;
+  if (part < 0 || !arrive_last(A, it, part, kvh, &s_last)) return;
+  join<E, D, kThreads>(A, it, part, kUnits, RT, kvh, &s_o[0][0][0]);
+}
 
-  // The work-group that finishes a tile's last chunk joins the chunks, in
-  // their order, whichever it is.  Its own wait makes a part's stores visible
-  // before its arrival is counted.
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-  wait_vm<0>();
-  __syncthreads();
-  const int chunks = (kv + chunk - 1) / chunk;
-  if (threadIdx.x == 0) {
-    int32_t* count = A.arrive + (int64_t)part * hkv + kvh;
-    const int before = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = before == chunks - 1;
-    if (s_last) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next layer
+// ------------------------------------------------------- requests of many rows
+// 128 rows on the same keys: tiles of 64 are converted to bf16 once, a unit of
+// 16 tokens by each wave, into LDS, while the tile before is multiplied with
+// v_mfma_f32_32x32x16_bf16, 32 rows per wave.  K lies by token, V by dim in the
+// token order of P's registers, both XOR-swizzled in 16-byte pieces against
+// the 64 banks.
+template <int NC>
+__global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A) {
+  constexpr int D = 32 * NC, kThreads = 256, kKeys = 64, kUnits = kWideRows / kUnit;
+  constexpr int kSteps = D / 16, kDims = D / 32;
+  constexpr int kKVar = D % 128 == 0 ? 8 : D % 64 == 0 ? 4 : 2;
+  __shared__ __attribute__((aligned(128))) uint8_t s_k[2][kKeys * D * 2], s_v[2][kKeys * D * 2];
+  __shared__ int s_bad[2][4];
+  __shared__ int s_last;
+  auto swz_k = [](int token, int piece) {
+    return D % 128 == 0 ? piece ^ (token & 15) : D % 64 == 0 ? piece ^ ((token >> 1) & 7) : piece ^ ((token >> 2) & 3);
+  };
+
+  const int hkv = A.cache.heads;
+  const int item = blockIdx.x / hkv, kvh = blockIdx.x - item * hkv;
+  Item it;
+  if (!read_item(A, 2, kCountWide, item, 0, kWideRows, it)) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
+  const int m16 = lane & 15, g = lane >> 4;
+  const int G = A.G, row_first = it.row0 + wave * 32;
+  const int row = min(row_first + n, it.nrows - 1), jq = row / G;
+  const bool live = row_first < it.nrows;
+  const int limit = min(it.pos0 + jq + 1, it.kv);
+  const int limit_first = uniform(min(it.pos0 + min(row_first, it.nrows - 1) / G + 1, it.kv));
+  const int limit_last = live ? uniform(min(it.pos0 + min(row_first + 31, it.nrows - 1) / G + 1, it.kv)) : 0;
+
+  bf16x8 qf[kSteps];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(A.q.p) + (int64_t)(it.qs + jq) * A.q.ts + (kvh * G + row - jq * G) * A.q.hs;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(q + 16 * s + 8 * h);
   }
-  __syncthreads();
-  if (!s_last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-  float* s_join = &s_o[0][0][0];
+
+  const int32_t* trow = A.table + (int64_t)it.seq * A.tstride;
+  const uint8_t* head = A.cache.base + ((int64_t)kvh << A.cache.bt_log2 >> 4) * (544 * NC);
+  const int unit_mask = (1 << (A.cache.bt_log2 - 4)) - 1;
+  const int n_tiles = (max(it.end - it.begin, 0) + kKeys - 1) / kKeys;
+  bool bad_block = false;
+
+  // Block ids of this wave's unit in 64 tiles, one per lane; -1 outside the cache.
+  auto fetch_ids = [&](int tile) {
+    const int token = it.begin + (tile + lane) * kKeys + kUnit * wave;
+    int id = 0;
+    if (token < it.end) {
+      id = trow[token >> A.cache.bt_log2];
+      if ((unsigned)id >= (unsigned)A.cache.blocks) id = -1, bad_block = true;
+    }
+    return id;
+  };
+  uint32_t kc[NC], vc[NC], vs[NC];
+  uint8_t ks[NC];
+  int raw_id = 0;  // block of the unit in kc .. vs
+  int ids = fetch_ids(0);
+  auto load = [&](int tile) {
+    if (tile && tile % 64 == 0) ids = fetch_ids(tile);
+    raw_id = __builtin_amdgcn_readlane(ids, tile % 64);
+    const int token = it.begin + tile * kKeys + kUnit * wave;
+    // behind the last token: the id is 0, a block of the cache
+    const uint8_t* rec = head + max(raw_id, 0) * A.cache.stride + ((token >> 4) & unit_mask) * (544 * NC);
+    load_unit<NC>(rec, lane, kc, vc, ks, vs);
+  };
+  // The unit in registers to bf16 in LDS.
+  auto convert = [&](int tile, int buf) {
+    const int token = it.begin + tile * kKeys + kUnit * wave;
+    if (lane == 0) s_bad[buf][wave] = raw_id < 0;
+    if (raw_id < 0 || token + kUnit > it.end) {
+      // bytes behind the last token may hold anything, a scale of NaN among it
+      uint32_t keep = 0;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int live = min(nrows - row0 - r * kUnit, kUnit);
-    if (live <= 0) break;
-    const int tasks = live * kVecs;
-    const int groups = max(1, min(kThreads / tasks, chunks));  // threads per task, each every groups-th chunk
-    for (int t0 = 0; t0 < tasks; t0 += kThreads) {  // more than one turn only with one group
-      const int grp = threadIdx.x / tasks, task = t0 + threadIdx.x - (groups > 1 ? grp * tasks : 0);
-      const int row = task / kVecs, d = (task - row * kVecs) * 4;
-      const bool work = task < tasks && (groups == 1 || grp < groups);
-      float M = kNone, L = 0.0f;
-      f4 acc{0, 0, 0, 0};
-      if (work) {
-        for (int c = groups > 1 ? grp : 0; c < chunks; c += 4 * groups) {
-          float2 ml[4], lo[4], hi[4];
+      for (int i = 0; i < 4; ++i)
+        if (raw_id >= 0 && token + 4 * g + i < it.end) keep |= 0xffu << (8 * i);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float* p = part_at(min(c + e * groups, chunks - 1), r);
-            ml[e] = get2(p + kUnit * D + 2 * row);
-            lo[e] = get2(p + row * D + d);
-            hi[e] = get2(p + row * D + d + 2);
-          }
+      for (int c = 0; c < NC; ++c) {
+        vc[c] &= keep;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (c + e * groups >= chunks) break;
-            const float mn = fmaxf(M, ml[e].x), a = exp2_hw(M - mn), b = exp2_hw(ml[e].x - mn);
-            M = mn;
-            L = L * a + ml[e].y * b;
-            acc = acc * a + b * f4{lo[e].x, lo[e].y, hi[e].x, hi[e].y};
-          }
-        }
+        for (int b = 0; b < 4; ++b)
+          if (!((keep >> (8 * ((4 * c + b) / NC))) & 1)) vs[c] &= ~(0xffu << (8 * b));
       }
-      if (groups > 1) {
-        __syncthreads();
-        if (work) {
-          float* s = s_join + threadIdx.x * 6;
-          s[0] = M, s[1] = L;
-          s[2] = acc[0], s[3] = acc[1], s[4] = acc[2], s[5] = acc[3];
-        }
-        __syncthreads();
-        if (work && grp == 0) {
-          for (int e = 1; e < groups; ++e) {
-            const float* s = s_join + (threadIdx.x + e * tasks) * 6;
-            const float mn = fmaxf(M, s[0]), a = exp2_hw(M - mn), b = exp2_hw(s[0] - mn);
-            M = mn;
-            L = L * a + s[1] * b;
-            acc = acc * a + b * f4{s[2], s[3], s[4], s[5]};
-          }
-        }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float sc = __uint_as_float((uint32_t)ks[c] << 23);
+      const int t = kUnit * wave + m16;
+      *reinterpret_cast<u32x4*>(s_k[buf] + t * (2 * D) + swz_k(t, 4 * c + g) * 16) =
+          u32x4{fp4_pair(kc[c], sc, 0), fp4_pair(kc[c], sc, 1), fp4_pair(kc[c], sc, 2), fp4_pair(kc[c], sc, 3)};
+      uint32_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = j * NC + c;
+        r[j] = fp4_pair(vc[c], byte_scale(vs[at >> 2], at & 3), j);
       }
-      if (work && grp == 0) store(r, row, d, acc, inverse(L));
-      if (groups > 1) break;
+      // tokens 4g..4g+3 of the unit, one dim: 8 bytes; the two halves of a
+      // 16-byte piece are the tokens 8 apart that one lane of P holds
+      const int piece = 2 * wave + (g & 1), half = (g >> 1) * 8;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int dim = 32 * c + 16 * e + m16;
+        const uint32_t sel = e ? 0x07060302u : 0x05040100u;
+        *reinterpret_cast<uint2*>(s_v[buf] + dim * (2 * kKeys) + ((piece ^ ((dim >> 1) & 7)) * 16) + half) =
+            make_uint2(__builtin_amdgcn_perm(r[1], r[0], sel), __builtin_amdgcn_perm(r[3], r[2], sel));
+      }
+    }
+  };
+
+  int k_at[kKVar], v_at[4];
+#pragma unroll
+  for (int c = 0; c < kKVar; ++c) k_at[c] = n * (2 * D) + swz_k(n, 2 * c + h) * 16;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v_at[c] = n * (2 * kKeys) + ((2 * c + h) ^ ((n >> 1) & 7)) * 16;
+
+  f16v o[kDims];
+#pragma unroll
+  for (int d = 0; d < kDims; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  float m = kNone, l = 0.0f;
+
+  auto compute = [&](int tile, int buf) {
+    const int key0 = it.begin + tile * kKeys;
+    const uint8_t *sk = s_k[buf], *sv = s_v[buf];
+    f16v s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) {
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(sk + k_at[c % kKVar] + u * 32 * (2 * D) + (c / kKVar) * (kKVar * 32));
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[c], s[u], 0, 0, 0);
+      }
+    const int bad0 = s_bad[buf][0], bad1 = s_bad[buf][1], bad2 = s_bad[buf][2], bad3 = s_bad[buf][3];
+    if (key0 + kKeys > limit_first || uniform(bad0 | bad1 | bad2 | bad3)) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int unit = 2 * u + (i >> 3);
+          const int bad = unit == 0 ? bad0 : unit == 1 ? bad1 : unit == 2 ? bad2 : bad3;
+          if (bad || key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3) >= limit) s[u][i] = -INFINITY;
+        }
+    }
+    float most = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) most = fmaxf(most, s[i >> 4][i & 15]);
+    most *= A.scale_log2e;
+    if (__any(most > m + kSlack)) {
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const float mn = fmaxf(m, most), alpha = exp2_hw(m - mn);
+      m = mn;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[d] *= alpha;
+    }
+    bf16x8 pf[4];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float p = exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
+      l += p;
+      pf[i >> 3][i & 7] = (__bf16)p;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) {
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(sv + v_at[c] + d * (32 * 2 * kKeys));
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pf[c], o[d], 0, 0, 0);
+      }
+  };
+
+  if (n_tiles > 0) {
+    load(0);
+    convert(0, 0);
+    if (n_tiles > 1) load(1);
+    for (int t = 0; t < n_tiles; ++t) {
+      __syncthreads();  // tile t is in LDS, and tile t-1's buffer is free
+      if (t + 1 < n_tiles) {
+        convert(t + 1, (t + 1) & 1);
+        if (t + 2 < n_tiles) load(t + 2);
+      }
+      if (it.begin + t * kKeys < limit_last) compute(t, t & 1);
     }
   }
+  if (__any(bad_block) && lane == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BLOCK_RANGE);
+
+  l += __shfl_xor(l, 32);
+  if (row_first + n < it.nrows) {
+    const float inv = inverse(l);
+    float* p = it.part < 0 ? nullptr : part_at<D>(A, it.part + it.ci * kUnits + 2 * wave + (n >> 4), kvh);
+#pragma unroll
+    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int dim = 32 * d + 2 * i + 4 * h;
+        const f4 acc{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+        if (it.part < 0) {
+          store_out<Bf16>(A, it, kvh, row, dim, acc, inv);
+        } else {
+          put2(p + (n & 15) * D + dim, acc[0], acc[1]);
+          put2(p + (n & 15) * D + dim + 2, acc[2], acc[3]);
+        }
+      }
+    if (it.part >= 0 && h == 0) put2(p + kUnit * D + 2 * (n & 15), m, l);
+  }
+  if (it.part < 0 || !arrive_last(A, it, it.part, kvh, &s_last)) return;
+  join<Bf16, D, kThreads>(A, it, it.part, kUnits, kUnits, kvh, reinterpret_cast<float*>(s_k));
 }
 
 template <class E, int NC>
-hipError_t launch(const AttendArgs& A, int blocks, bool wide, hipStream_t s) {
+hipError_t launch(const AttendArgs& A, int blocks, bool many, hipStream_t s) {
   // 8 waves join through 64 KB of LDS at 128 dims; past that, 4
   constexpr int W = NC <= 4 ? 8 : 4;
-  if (wide) attend_kernel<E, NC, 2, W><<<blocks, 64 * W, 0, s>>>(A);
-  attend_kernel<E, NC, 1, W><<<blocks, 64 * W, 0, s>>>(A);
+  if (many) {
+    if constexpr (sizeof(typename E::T) == 2) attend_wide_kernel<NC><<<blocks, 256, 0, s>>>(A);
+    else attend_kernel<E, NC, 2, 2, W><<<blocks * (kWideRows / kMidRows), 64 * W, 0, s>>>(A);
+    attend_kernel<E, NC, 2, 1, W><<<blocks, 64 * W, 0, s>>>(A);
+  }
+  attend_kernel<E, NC, 1, 0, W><<<blocks, 64 * W, 0, s>>>(A);
   return hipGetLastError();
 }
 
 template <class E>
-hipError_t launch_nc(const AttendArgs& A, int blocks, bool wide, hipStream_t s) {
+hipError_t launch_nc(const AttendArgs& A, int blocks, bool many, hipStream_t s) {
   switch (A.cache.nc) {
-    case 1: return launch<E, 1>(A, blocks, wide, s);
-    case 2: return launch<E, 2>(A, blocks, wide, s);
-    case 3: return launch<E, 3>(A, blocks, wide, s);
-    case 4: return launch<E, 4>(A, blocks, wide, s);
-    case 5: return launch<E, 5>(A, blocks, wide, s);
-    case 6: return launch<E, 6>(A, blocks, wide, s);
-    case 7: return launch<E, 7>(A, blocks, wide, s);
-    default: return launch<E, 8>(A, blocks, wide, s);
+    case 1: return launch<E, 1>(A, blocks, many, s);
+    case 2: return launch<E, 2>(A, blocks, many, s);
+    case 3: return launch<E, 3>(A, blocks, many, s);
+    case 4: return launch<E, 4>(A, blocks, many, s);
+    case 5: return launch<E, 5>(A, blocks, many, s);
+    case 6: return launch<E, 6>(A, blocks, many, s);
+    case 7: return launch<E, 7>(A, blocks, many, s);
+    default: return launch<E, 8>(A, blocks, many, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, bool wide, hipStream_t s) {
-  return dtype == LORA_DTYPE_BF16 ? launch_nc<Bf16>(A, blocks, wide, s) : launch_nc<F32>(A, blocks, wide, s);
+hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, bool many, hipStream_t s) {
+  return dtype == LORA_DTYPE_BF16 ? launch_nc<Bf16>(A, blocks, many, s) : launch_nc<F32>(A, blocks, many, s);
 }
 
 }  // namespace kv

@@ -88,30 +88,33 @@ __device__ __forceinline__ Request request(const BuildArgs& A, int i, int cap) {
   return r;
 }
 
-__device__ __forceinline__ int tiles_of(int tokens, int G, int rows) {
-  return (int)(((int64_t)tokens * G + rows - 1) / rows);
+__device__ __forceinline__ int class_of(int rows, bool many) { return rows <= kUnit || !many ? 0 : rows <= kMidMost ? 1 : 2; }
+__device__ __forceinline__ int tiles_of(int rows, int cls) {
+  const int per = rows_of_class(cls);
+  return (rows + per - 1) / per;
 }
 
 __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
-  __shared__ uint32_t s_a[kWavesB][8], s_b[kWavesB][8];
+  __shared__ uint32_t s_a[kWavesB][8], s_b[kWavesB][8], s_c[kWavesB][8];
   __shared__ int64_t s_read[kWavesB];
   __shared__ int32_t s_row[kTurn];    // first token row
   __shared__ int32_t s_fresh[kTurn];  // first new block, counted over the step
-  __shared__ int32_t s_item[kTurn];   // first work item
-  __shared__ int32_t s_wide[kTurn];   // first work item of 32 rows
-  __shared__ int32_t s_ctx[kTurn], s_chunks[kTurn], s_part[kTurn];
+  __shared__ int32_t s_item[kClasses][kTurn];  // first work item of its class
+  __shared__ int32_t s_ctx[kTurn], s_chunks[kTurn], s_part[kTurn], s_kv[kTurn], s_rows[kTurn];
   const int tid = threadIdx.x, wg = blockIdx.x, nwg = gridDim.x;
   const int bt = 1 << A.bt_log2;
   const int cap = (int)min((int64_t)A.width << A.bt_log2, (int64_t)0x7fffffff);
 
   // Tokens per work item, from the cached tokens that all row tiles read.
+  const bool many = many_rows(A.T, A.B);
   Request r[kPer];
   int64_t mine = 0;
   for (int base = 0; base < A.B; base += kTurn) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       r[e] = request(A, base + tid * kPer + e, cap);
-      mine += (int64_t)tiles_of(r[e].add, A.G, kUnit) * min((int64_t)r[e].ctx + r[e].add, (int64_t)cap);
+      const int rows = r[e].add * A.G;
+      mine += (int64_t)tiles_of(rows, class_of(rows, many)) * min((int64_t)r[e].ctx + r[e].add, (int64_t)cap);
     }
   }
 #pragma unroll
@@ -123,8 +126,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   const int64_t rounded = max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)kMinChunk);
   const int chunk = (int)min(rounded, (int64_t)1 << 30);
 
-  const bool wide_ok = wide_step(A.T, A.B);
-  int64_t rows0 = 0, fresh0 = 0, items0 = 0, wide0 = 0, parts0 = 0;
+  int64_t rows0 = 0, fresh0 = 0, parts0 = 0, items0[kClasses] = {0, 0, 0};
   int flags = 0;
   for (int base = 0; base < A.B; base += kTurn) {
     if (A.B > kTurn) {  // else the first pass left them here
@@ -136,8 +138,8 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
     for (int e = 0; e < kPer; ++e) x[0] += r[e].add, x[1] += r[e].need - r[e].have;
     int64_t at[2], sum[2];
     block_scan<2>(x, at, sum, s_a);
-    int first[kPer], last[kPer], kv[kPer], n_items[kPer], n_wide[kPer], n_parts[kPer], chunks[kPer];
-    uint32_t y[3] = {0, 0, 0};
+    int first[kPer], last[kPer], kv[kPer], cls[kPer], tiles[kPer], chunks[kPer];
+    uint32_t y[1] = {0};
     int64_t row = rows0 + at[0], fresh = fresh0 + at[1];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -149,13 +151,11 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       s_fresh[tid * kPer + e] = (int)min(fresh, (int64_t)0x7fffffff);
       fresh += want;
       kv[e] = (int)min(min((int64_t)r[e].ctx + (last[e] - first[e]), (int64_t)cap), (int64_t)(r[e].have + got) << A.bt_log2);
-      const bool wide = wide_ok && (int64_t)(last[e] - first[e]) * A.G > kUnit;
+      const int rows = i < A.B ? (last[e] - first[e]) * A.G : 0;
+      cls[e] = class_of(rows, many);
+      tiles[e] = tiles_of(rows, cls[e]);
       chunks[e] = max((int)(((int64_t)kv[e] + chunk - 1) / chunk), 1);
-      const int n = i < A.B ? tiles_of(last[e] - first[e], A.G, wide ? 2 * kUnit : kUnit) * chunks[e] : 0;
-      n_items[e] = wide ? 0 : n;
-      n_wide[e] = wide ? n : 0;
-      n_parts[e] = chunks[e] > 1 ? n_items[e] + 2 * n_wide[e] : 0;
-      y[0] += n_items[e], y[1] += n_wide[e], y[2] += n_parts[e];
+      if (chunks[e] > 1) y[0] += tiles[e] * chunks[e] * (rows_of_class(cls[e]) / kUnit);
       if (wg == 0 && i < A.B) {
         A.q_indptr[i] = first[e];
         A.kv_len[i] = kv[e];
@@ -168,19 +168,36 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
           flags |= LORA_KV_FLAG_BLOCK_RANGE;
       }
     }
-    int64_t at2[3], sum2[3];
-    block_scan<3>(y, at2, sum2, s_b);
-    int64_t item = items0 + at2[0], wide = wide0 + at2[1], part = parts0 + at2[2];
+    int64_t at2[1], sum2[1], at3[3], sum3[3];
+    block_scan<1>(y, at2, sum2, s_b);
+    int64_t part = parts0 + at2[0];
+    uint32_t z[3] = {0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int k = tid * kPer + e;
+      s_part[k] = -1;
+      if (chunks[e] > 1) {
+        const int64_t need = (int64_t)tiles[e] * chunks[e] * (rows_of_class(cls[e]) / kUnit);
+        if (part + need <= A.part_cap) s_part[k] = (int)part;
+        else chunks[e] = 1;
+        part += need;
+      }
+      z[cls[e]] += tiles[e] * chunks[e];
+    }
+    block_scan<3>(z, at3, sum3, s_c);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int k = tid * kPer + e;
       s_row[k] = first[e];
-      s_item[k] = (int)item;
-      s_wide[k] = (int)wide;
       s_ctx[k] = r[e].ctx;
+      s_kv[k] = kv[e];
+      s_rows[k] = (last[e] - first[e]) * A.G;
       s_chunks[k] = chunks[e];
-      s_part[k] = chunks[e] > 1 ? (int)part : -1;
-      item += n_items[e], wide += n_wide[e], part += n_parts[e];
+#pragma unroll
+      for (int c = 0; c < kClasses; ++c) {
+        s_item[c][k] = (int)(items0[c] + at3[c]);
+        at3[c] += cls[e] == c ? tiles[e] * chunks[e] : 0;
+      }
     }
     __syncthreads();
     const int n = min(kTurn, A.B - base);
@@ -216,28 +233,26 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       for (int64_t f = fresh0 + tid; f < min(fresh1, (int64_t)A.nfree); f += kThreads)
         if ((unsigned)A.free_blocks[f] >= (unsigned)A.blocks) flags |= LORA_KV_FLAG_BLOCK_RANGE;
     }
-    // One item: its request, tile, chunk and the tile's first part (-1: alone).
-    auto fill = [&](const int32_t* start, int w, int units, int4* to) {
-      const int k = bisect(start, n, w);
-      const int local = w - start[k], tile = local / s_chunks[k], c = local - tile * s_chunks[k];
-      int part = -1;
-      if (s_part[k] >= 0) {
-        part = s_part[k] + tile * s_chunks[k] * units;
-        if (part + s_chunks[k] * units > A.part_cap) part = -1;
-        if (part >= 0)
-          for (int h = 0; c == 0 && h < A.hkv; ++h) A.arrive[(int64_t)part * A.hkv + h] = 0;
+    for (int c = 0; c < kClasses; ++c) {
+      const int units = rows_of_class(c) / kUnit;
+      for (int w = (int)items0[c] + wg * kThreads + tid; w < min(items0[c] + sum3[c], (int64_t)A.item_cap); w += nwg * kThreads) {
+        const int k = bisect(s_item[c], n, w);
+        const int local = w - s_item[c][k], tile = local / s_chunks[k], ci = local - tile * s_chunks[k];
+        int part = s_part[k];
+        if (part >= 0) {
+          part += tile * s_chunks[k] * units;
+          if (ci == 0)
+            for (int h = 0; h < A.hkv * units; ++h) A.arrive[(int64_t)part * A.hkv + h] = 0;
+        }
+        int4* to = A.items + 2 * ((int64_t)c * A.item_cap + w);
+        to[0] = make_int4(base + k, tile * rows_of_class(c), ci, part);
+        to[1] = make_int4(s_row[k], s_rows[k], s_ctx[k], s_kv[k]);
       }
-      *to = make_int4(base + k, tile, c, part);
-    };
-    for (int w = (int)items0 + wg * kThreads + tid; w < min(items0 + sum2[0], (int64_t)A.item_cap); w += nwg * kThreads)
-      fill(s_item, w, 1, A.items + w);
-    for (int w = (int)wide0 + wg * kThreads + tid; w < min(wide0 + sum2[1], (int64_t)A.item_cap); w += nwg * kThreads)
-      fill(s_wide, w, 2, A.items + A.item_cap + w);
+    }
     rows0 += sum[0];
     fresh0 += sum[1];
-    items0 += sum2[0];
-    wide0 += sum2[1];
-    parts0 += sum2[2];
+    parts0 += sum2[0];
+    for (int c = 0; c < kClasses; ++c) items0[c] += sum3[c];
     __syncthreads();
   }
 
@@ -259,14 +274,15 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       int v = 0;
       if (tid == kCountTokens) v = used;
       if (tid == kCountNewBlocks) v = (int)min(fresh0, (int64_t)0x7fffffff);
-      if (tid == kCountItems) v = (int)items0;
-      if (tid == kCountParts) v = (int)parts0;
-      if (tid == kCountWide) v = (int)wide0;
+      if (tid == kCountItems) v = (int)items0[0];
+      if (tid == kCountParts) v = (int)min(parts0, (int64_t)0x7fffffff);
+      if (tid == kCountMid) v = (int)items0[1];
+      if (tid == kCountWide) v = (int)items0[2];
       if (tid == kCountChunk) v = chunk;
       if (tid == kCountFlags) v = all;
       if (tid == kCountB) v = A.B;
       if (tid == kCountT) v = A.T;
-      if (tid == kCountCheck) v = check_word(A.B, A.T, (int)items0, (int)wide0, (int)parts0);
+      if (tid == kCountCheck) v = check_word(A.B, A.T, (int)items0[0], (int)items0[1], (int)items0[2], (int)min(parts0, (int64_t)0x7fffffff));
       A.counts[tid] = v;
     }
     if (tid == kThreads - 1) A.q_indptr[A.B] = used;

@@ -15,40 +15,49 @@ constexpr int kMinChunk = 1024;   // smallest chunk of cached tokens per work it
 constexpr int kTargetItems = 1024;
 
 constexpr int kCountTokens = 0, kCountNewBlocks = 1, kCountItems = 2, kCountParts = 3, kCountChunk = 4,
-              kCountWide = 5, kCountFlags = 8, kCountB = 9, kCountT = 10, kCountCheck = 11, kNumCounts = 16;
+              kCountMid = 5, kCountWide = 6, kCountFlags = 8, kCountB = 9, kCountT = 10, kCountCheck = 11,
+              kNumCounts = 16;
 
+// Work items by class of their request's rows (new tokens x query heads per
+// kv head): up to 16 rows, one matrix tile; up to 64, two tiles on the same
+// converted keys; more, 128 rows that share the conversion through LDS.  The
+// last two only where a step brings more tokens than requests (what the host
+// knows of it, so that a decode step launches one kernel).
+constexpr int kClasses = 3;
+constexpr int kMidRows = 32, kWideRows = 128, kMidMost = 64;
 #if defined(__HIPCC__)
-__host__ __device__
+#define LORA_KV_HD __host__ __device__
+#else
+#define LORA_KV_HD
 #endif
-inline int32_t check_word(int32_t B, int32_t T, int32_t items, int32_t wide, int32_t parts) {
+LORA_KV_HD inline bool many_rows(int32_t T, int32_t B) { return T > B; }
+LORA_KV_HD inline int rows_of_class(int c) { return c == 0 ? kUnit : c == 1 ? kMidRows : kWideRows; }
+
+LORA_KV_HD inline int32_t check_word(int32_t B, int32_t T, int32_t items, int32_t mid, int32_t wide, int32_t parts) {
   uint32_t h = 0x4b56u;
   h = (h ^ (uint32_t)B) * 0x9e3779b1u;
   h = (h ^ (uint32_t)T) * 0x85ebca77u;
   h = (h ^ (uint32_t)items) * 0xc2b2ae3du;
-  h = (h ^ (uint32_t)wide) * 0x165667b1u;
+  h = (h ^ (uint32_t)mid) * 0x165667b1u;
+  h = (h ^ (uint32_t)wide) * 0x9e3779b1u;
   h = (h ^ (uint32_t)parts) * 0x27d4eb2fu;
   return (int32_t)(h ^ (h >> 15));
 }
 
-// Requests of more than 16 rows (new tokens x query heads per kv head) take
-// tiles of 32 rows, in a list of their own, where a step brings more tokens
-// than requests (what the host knows of it).
-#if defined(__HIPCC__)
-__host__ __device__
-#endif
-inline bool wide_step(int32_t T, int32_t B) { return T > B; }
-
-// Most work items of a step, in either list: sum of tiles_i * ceil(kv_i /
-// chunk) <= sum(tiles_i kv_i) / chunk + sum(tiles_i), the first term at most
+// Most work items of a class: sum of tiles_i * ceil(kv_i / chunk) <=
+// sum(tiles_i kv_i) / chunk + sum(tiles_i), the first term at most
 // kTargetItems / hkv by the choice of the chunk, tiles_i <= new_i G / 16 + 1.
 inline int64_t item_cap(int64_t T, int64_t B, int64_t hkv, int64_t G) {
   return kTargetItems / hkv + 1 + T * G / kUnit + 1 + B;
 }
-// Most parts (16 rows each) of items that share their tile with others:
-// ceil(kv / chunk) < 2 kv / chunk of them for each 16 rows, and tiles of 32
-// rows have at most half as many 16 rows again as the choice of the chunk
-// counts.
-inline int64_t part_cap(int64_t hkv) { return 3 * (kTargetItems / hkv + 1); }
+// Room for partial results (16 rows of one chunk each).  A decode step needs
+// at most 2 (kTargetItems / hkv + 1) of them; requests of many rows whose
+// parts find no room are not split.
+inline int64_t part_cap(int64_t hkv) { return 8 * (kTargetItems / hkv + 1); }
+
+// An item is two int4: {request, first row, chunk, first part of the tile or
+// -1 (not split)} and {first token row, rows of the request, position of its
+// first token, cached tokens}.
 
 }  // namespace kv
 }  // namespace lora

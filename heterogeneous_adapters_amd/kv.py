@@ -22,7 +22,8 @@ from . import lora
 
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 SCALING_NONE, SCALING_LINEAR, SCALING_NTK, SCALING_YARN, SCALING_BANDS = range(5)
-COUNT_TOKENS, COUNT_NEW_BLOCKS, COUNT_ITEMS, COUNT_PARTS, COUNT_CHUNK, COUNT_WIDE, COUNT_FLAGS = 0, 1, 2, 3, 4, 5, 8
+COUNT_TOKENS, COUNT_NEW_BLOCKS, COUNT_ITEMS, COUNT_PARTS, COUNT_CHUNK, COUNT_MID, COUNT_WIDE = range(7)
+COUNT_FLAGS = 8
 FLAG_LENGTH, FLAG_TOKENS, FLAG_FREE_LIST, FLAG_BLOCK_RANGE, FLAG_NONFINITE, FLAG_BATCH = 1, 2, 4, 8, 16, 32
 N_COUNTS = 16
 MAX_SEQS = 1 << 16

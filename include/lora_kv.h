@@ -110,7 +110,8 @@ typedef struct {
 #define LORA_KV_COUNT_ITEMS 2      /* work items of 16 rows (per kv head) */
 #define LORA_KV_COUNT_PARTS 3      /* partial results (16 rows of one chunk each) */
 #define LORA_KV_COUNT_CHUNK 4      /* cached tokens per work item */
-#define LORA_KV_COUNT_WIDE 5       /* work items of 32 rows (per kv head) */
+#define LORA_KV_COUNT_MID 5        /* work items of 32 rows (per kv head) */
+#define LORA_KV_COUNT_WIDE 6       /* work items of 128 rows (per kv head) */
 #define LORA_KV_COUNT_FLAGS 8
 #define LORA_KV_FLAG_LENGTH 1     /* a negative length, or one past the table's row (cut) */
 #define LORA_KV_FLAG_TOKENS 2     /* more new tokens than the call's T (the rest has no rows) */
@@ -122,7 +123,7 @@ typedef struct {
 /* Bytes of the buffer (0 outside the limits: max_tokens in [0,
  * LORA_MAX_TOKENS], max_seqs in [1, LORA_KV_MAX_SEQS], num_q_heads a multiple
  * of num_kv_heads up to LORA_KV_MAX_HEADS, head_dim as in the cache, and
- * max_tokens * num_q_heads / 16 + max_seqs * num_kv_heads + 8192 < 2^23 work
+ * max_tokens * num_q_heads / 16 + max_seqs * num_kv_heads + 8192 < 2^21 work
  * items). */
 size_t lora_kv_batch_size(int32_t max_tokens, int32_t max_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                           int32_t head_dim);

@@ -176,7 +176,8 @@ def test_a_split_request_gives_the_same_bits_every_time():
 def test_split_requests_with_many_new_tokens(ctx, new, hq, hkv, D, dtype):
     s = Step(40 + D, np.array(ctx), np.array(new), hq, hkv, D, 16, dtype, pad=2)
     got = s.run(1.0 / math.sqrt(D))
-    assert int(s.batch.counts[kv.COUNT_PARTS]) > 1 and int(s.batch.counts[kv.COUNT_WIDE]) > 0
+    c = s.batch.counts
+    assert int(c[kv.COUNT_PARTS]) > 1 and int(c[kv.COUNT_MID]) + int(c[kv.COUNT_WIDE]) > 0
     s.check(got, 1.0 / math.sqrt(D))
 
 

@@ -26,7 +26,7 @@ def test_binding_constants_match_header():
     defs = dict(re.findall(r"^#define (LORA_[A-Z_0-9]+) \(?([^/\n]*?)\)?\s*(?:/\*.*)?$", open(HEADER).read(), flags=re.M))
     want = {"LORA_KV_MAX_SEQS": kv.MAX_SEQS, "LORA_ROPE_HALF": kv.ROPE_HALF, "LORA_ROPE_INTERLEAVED": kv.ROPE_INTERLEAVED}
     want.update({f"LORA_KV_COUNT_{n}": getattr(kv, f"COUNT_{n}")
-                 for n in ("TOKENS", "NEW_BLOCKS", "ITEMS", "PARTS", "CHUNK", "WIDE", "FLAGS")})
+                 for n in ("TOKENS", "NEW_BLOCKS", "ITEMS", "PARTS", "CHUNK", "MID", "WIDE", "FLAGS")})
     want.update({f"LORA_KV_FLAG_{n}": getattr(kv, f"FLAG_{n}")
                  for n in ("LENGTH", "TOKENS", "FREE_LIST", "BLOCK_RANGE", "NONFINITE", "BATCH")})
     want.update({f"LORA_ROPE_SCALING_{n}": getattr(kv, f"SCALING_{n}") for n in ("NONE", "LINEAR", "NTK", "YARN", "BANDS")})
