@@ -375,8 +375,7 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
   A.cache = cache_of(cache);
   A.scale_log2e = scale * 1.4426950408889634f;
   A.part = static_cast<float*>(ws);
-  const int64_t blocks = item_cap(T, B, batch->num_kv_heads, A.G) * batch->num_kv_heads;
-  return hip(launch_attend(A, dtype, (int)blocks, many_rows(T, B), static_cast<hipStream_t>(stream)));
+  return hip(launch_attend(A, dtype, many_rows(T, B), static_cast<hipStream_t>(stream)));
 }
 
 lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, const lora_heads_t* v,

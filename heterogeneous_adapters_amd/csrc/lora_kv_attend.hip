@@ -15,6 +15,8 @@
 // tokens 4g..4g+3 of each 16) is the B operand that O^T = V^T P^T needs, with
 // the record's V order supplying A, so P never leaves its registers.  fp32
 // rows are split into three bf16 terms (24 bits), the codes being exact.
+#include <type_traits>
+
 #include "lora_kv_dev.h"
 #include "lora_kv_host.h"
 
@@ -108,7 +110,6 @@ struct Item {
 __device__ __forceinline__ bool read_item(const AttendArgs& A, int cls, int count_at, int item, int skip, int rows, Item& it) {
   const int4* d = A.items + 2 * ((int64_t)cls * A.item_cap + item);
   const int4 x = d[0], y = d[1];
-  const int chunk = A.counts[kCountChunk];
   if (!plan_ok(A)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
     return false;
@@ -118,6 +119,7 @@ __device__ __forceinline__ bool read_item(const AttendArgs& A, int cls, int coun
   it.qs = uniform(y.x), it.nrows = uniform(y.y), it.pos0 = uniform(y.z), it.kv = uniform(y.w);
   if (it.row0 >= it.nrows) return false;
   const int sees = min(it.pos0 + min(it.row0 + rows - 1, it.nrows - 1) / A.G + 1, it.kv);
+  const int chunk = even_chunk(it.kv, A.counts[cls == 2 ? kCountChunkWide : kCountChunk]);
   it.begin = it.part < 0 ? 0 : it.ci * chunk;
   it.end = it.part < 0 ? sees : min(it.begin + chunk, sees);
   it.chunks = it.part < 0 ? 1 : (it.kv + chunk - 1) / chunk;
@@ -476,7 +478,7 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
   constexpr int kSteps = D / 16, kDims = D / 32;
   constexpr int kKVar = D % 128 == 0 ? 8 : D % 64 == 0 ? 4 : 2;
   __shared__ __attribute__((aligned(128))) uint8_t s_k[2][kKeys * D * 2], s_v[2][kKeys * D * 2];
-  __shared__ int s_bad[2][4];
+  __shared__ __attribute__((aligned(4))) uint8_t s_bad[2][4];  // a tile's units whose block is outside the cache
   __shared__ int s_last;
   auto swz_k = [](int token, int piece) {
     return D % 128 == 0 ? piece ^ (token & 15) : D % 64 == 0 ? piece ^ ((token >> 1) & 7) : piece ^ ((token >> 2) & 3);
@@ -531,7 +533,8 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
     load_unit<NC>(rec, lane, kc, vc, ks, vs);
   };
   // The unit in registers to bf16 in LDS.
-  auto convert = [&](int tile, int buf) {
+  auto convert = [&](int tile, auto which) {
+    constexpr int buf = which;
     const int token = it.begin + tile * kKeys + kUnit * wave;
     if (lane == 0) s_bad[buf][wave] = raw_id < 0;
     if (raw_id < 0 || token + kUnit > it.end) {
@@ -586,9 +589,11 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = kNone, l = 0.0f;
 
-  auto compute = [&](int tile, int buf) {
+  auto compute = [&](int tile, auto which) {
+    constexpr int buf = which;
     const int key0 = it.begin + tile * kKeys;
     const uint8_t *sk = s_k[buf], *sv = s_v[buf];
+    const uint32_t bad_units = *reinterpret_cast<const uint32_t*>(s_bad[buf]);
     f16v s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -601,15 +606,22 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
         const bf16x8 a = *reinterpret_cast<const bf16x8*>(sk + k_at[c % kKVar] + u * 32 * (2 * D) + (c / kKVar) * (kKVar * 32));
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[c], s[u], 0, 0, 0);
       }
-    const int bad0 = s_bad[buf][0], bad1 = s_bad[buf][1], bad2 = s_bad[buf][2], bad3 = s_bad[buf][3];
-    if (key0 + kKeys > limit_first || uniform(bad0 | bad1 | bad2 | bad3)) {
+    // reads six ahead of their products
+    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+    for (int i = 0; i < kSteps * 2 - 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
+    const uint32_t bad = (uint32_t)uniform((int)bad_units);
+    if (key0 + kKeys > limit_first || bad) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int unit = 2 * u + (i >> 3);
-          const int bad = unit == 0 ? bad0 : unit == 1 ? bad1 : unit == 2 ? bad2 : bad3;
-          if (bad || key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3) >= limit) s[u][i] = -INFINITY;
+          const int hide = (bad >> (8 * (2 * u + (i >> 3)))) & 1 ? 0x40000000 : 0;
+          if (key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3) + hide >= limit) s[u][i] = -INFINITY;
         }
     }
     float most = s[0][0];
@@ -641,16 +653,22 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
   };
 
   if (n_tiles > 0) {
-    load(0);
-    convert(0, 0);
-    if (n_tiles > 1) load(1);
-    for (int t = 0; t < n_tiles; ++t) {
+    const std::integral_constant<int, 0> zero;
+    const std::integral_constant<int, 1> one;
+    auto turn = [&](int t, auto mine, auto other) {
       __syncthreads();  // tile t is in LDS, and tile t-1's buffer is free
       if (t + 1 < n_tiles) {
-        convert(t + 1, (t + 1) & 1);
+        convert(t + 1, other);
         if (t + 2 < n_tiles) load(t + 2);
       }
-      if (it.begin + t * kKeys < limit_last) compute(t, t & 1);
+      if (it.begin + t * kKeys < limit_last) compute(t, mine);
+    };
+    load(0);
+    convert(0, zero);
+    if (n_tiles > 1) load(1);
+    for (int t = 0; t < n_tiles; t += 2) {
+      turn(t, zero, one);
+      if (t + 1 < n_tiles) turn(t + 1, one, zero);
     }
   }
   if (__any(bad_block) && lane == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BLOCK_RANGE);
@@ -679,36 +697,37 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
 }
 
 template <class E, int NC>
-hipError_t launch(const AttendArgs& A, int blocks, bool many, hipStream_t s) {
+hipError_t launch(const AttendArgs& A, bool many, hipStream_t s) {
   // 8 waves join through 64 KB of LDS at 128 dims; past that, 4
   constexpr int W = NC <= 4 ? 8 : 4;
+  auto blocks = [&](int c) { return (unsigned)(class_cap(c, A.T, A.B, A.cache.heads, A.G) * A.cache.heads); };
   if (many) {
-    if constexpr (sizeof(typename E::T) == 2) attend_wide_kernel<NC><<<blocks, 256, 0, s>>>(A);
-    else attend_kernel<E, NC, 2, 2, W><<<blocks * (kWideRows / kMidRows), 64 * W, 0, s>>>(A);
-    attend_kernel<E, NC, 2, 1, W><<<blocks, 64 * W, 0, s>>>(A);
+    if constexpr (sizeof(typename E::T) == 2) attend_wide_kernel<NC><<<blocks(2), 256, 0, s>>>(A);
+    else attend_kernel<E, NC, 2, 2, W><<<blocks(2) * (kWideRows / kMidRows), 64 * W, 0, s>>>(A);
+    attend_kernel<E, NC, 2, 1, W><<<blocks(1), 64 * W, 0, s>>>(A);
   }
-  attend_kernel<E, NC, 1, 0, W><<<blocks, 64 * W, 0, s>>>(A);
+  attend_kernel<E, NC, 1, 0, W><<<blocks(0), 64 * W, 0, s>>>(A);
   return hipGetLastError();
 }
 
 template <class E>
-hipError_t launch_nc(const AttendArgs& A, int blocks, bool many, hipStream_t s) {
+hipError_t launch_nc(const AttendArgs& A, bool many, hipStream_t s) {
   switch (A.cache.nc) {
-    case 1: return launch<E, 1>(A, blocks, many, s);
-    case 2: return launch<E, 2>(A, blocks, many, s);
-    case 3: return launch<E, 3>(A, blocks, many, s);
-    case 4: return launch<E, 4>(A, blocks, many, s);
-    case 5: return launch<E, 5>(A, blocks, many, s);
-    case 6: return launch<E, 6>(A, blocks, many, s);
-    case 7: return launch<E, 7>(A, blocks, many, s);
-    default: return launch<E, 8>(A, blocks, many, s);
+    case 1: return launch<E, 1>(A, many, s);
+    case 2: return launch<E, 2>(A, many, s);
+    case 3: return launch<E, 3>(A, many, s);
+    case 4: return launch<E, 4>(A, many, s);
+    case 5: return launch<E, 5>(A, many, s);
+    case 6: return launch<E, 6>(A, many, s);
+    case 7: return launch<E, 7>(A, many, s);
+    default: return launch<E, 8>(A, many, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_attend(const AttendArgs& A, int dtype, int blocks, bool many, hipStream_t s) {
-  return dtype == LORA_DTYPE_BF16 ? launch_nc<Bf16>(A, blocks, many, s) : launch_nc<F32>(A, blocks, many, s);
+hipError_t launch_attend(const AttendArgs& A, int dtype, bool many, hipStream_t s) {
+  return dtype == LORA_DTYPE_BF16 ? launch_nc<Bf16>(A, many, s) : launch_nc<F32>(A, many, s);
 }
 
 }  // namespace kv

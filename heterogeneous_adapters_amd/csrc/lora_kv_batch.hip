@@ -16,8 +16,6 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 4;  // requests per thread and turn
-constexpr int kTurn = kThreads * kPer;
 constexpr int kWavesB = kThreads / 64;
 
 // Inclusive sums over a wave: within rows of 16 lanes, then from row to row.
@@ -94,9 +92,12 @@ __device__ __forceinline__ int tiles_of(int rows, int cls) {
   return (rows + per - 1) / per;
 }
 
+// kPer: requests per thread and turn.
+template <int kPer>
 __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
+  constexpr int kTurn = kThreads * kPer;
   __shared__ uint32_t s_a[kWavesB][8], s_b[kWavesB][8], s_c[kWavesB][8];
-  __shared__ int64_t s_read[kWavesB];
+  __shared__ int64_t s_read[2][kWavesB];
   __shared__ int32_t s_row[kTurn];    // first token row
   __shared__ int32_t s_fresh[kTurn];  // first new block, counted over the step
   __shared__ int32_t s_item[kClasses][kTurn];  // first work item of its class
@@ -108,23 +109,30 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   // Tokens per work item, from the cached tokens that all row tiles read.
   const bool many = many_rows(A.T, A.B);
   Request r[kPer];
-  int64_t mine = 0;
+  int64_t mine = 0, mine_wide = 0;
   for (int base = 0; base < A.B; base += kTurn) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       r[e] = request(A, base + tid * kPer + e, cap);
-      const int rows = r[e].add * A.G;
-      mine += (int64_t)tiles_of(rows, class_of(rows, many)) * min((int64_t)r[e].ctx + r[e].add, (int64_t)cap);
+      const int rows = r[e].add * A.G, cls = class_of(rows, many);
+      const int64_t reads = (int64_t)tiles_of(rows, cls) * min((int64_t)r[e].ctx + r[e].add, (int64_t)cap);
+      mine += cls == 2 ? 0 : reads;
+      mine_wide += cls == 2 ? reads : 0;
     }
   }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) mine += __shfl_xor(mine, d);
-  if ((tid & 63) == 0) s_read[tid >> 6] = mine;
+  for (int d = 32; d; d >>= 1) {
+    mine += __shfl_xor(mine, d);
+    if (many) mine_wide += __shfl_xor(mine_wide, d);
+  }
+  if ((tid & 63) == 0) s_read[0][tid >> 6] = mine, s_read[1][tid >> 6] = mine_wide;
   __syncthreads();
-  const int64_t read = s_read[0] + s_read[1] + s_read[2] + s_read[3];
-  const int64_t per = (read * A.hkv + kTargetItems - 1) / kTargetItems;
-  const int64_t rounded = max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)kMinChunk);
-  const int chunk = (int)min(rounded, (int64_t)1 << 30);
+  auto chunk_for = [&](const int64_t* reads, int target) {
+    const int64_t per = ((reads[0] + reads[1] + reads[2] + reads[3]) * A.hkv + target - 1) / target;
+    const int64_t rounded = max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)kMinChunk);
+    return (int)min(rounded, (int64_t)1 << 29);
+  };
+  const int chunk = chunk_for(s_read[0], kTargetItems), chunk_wide = chunk_for(s_read[1], kTargetWide);
 
   int64_t rows0 = 0, fresh0 = 0, parts0 = 0, items0[kClasses] = {0, 0, 0};
   int flags = 0;
@@ -138,6 +146,14 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
     for (int e = 0; e < kPer; ++e) x[0] += r[e].add, x[1] += r[e].need - r[e].have;
     int64_t at[2], sum[2];
     block_scan<2>(x, at, sum, s_a);
+    // the one cached block of each request that new tokens may lie in
+    int open_block[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int i = base + tid * kPer + e;
+      open_block[e] = 0;
+      if (wg == 0 && i < A.B && (r[e].ctx & (bt - 1)) != 0) open_block[e] = A.table[i * A.tstride + (r[e].ctx >> A.bt_log2)];
+    }
     int first[kPer], last[kPer], kv[kPer], cls[kPer], tiles[kPer], chunks[kPer];
     uint32_t y[1] = {0};
     int64_t row = rows0 + at[0], fresh = fresh0 + at[1];
@@ -152,9 +168,10 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       fresh += want;
       kv[e] = (int)min(min((int64_t)r[e].ctx + (last[e] - first[e]), (int64_t)cap), (int64_t)(r[e].have + got) << A.bt_log2);
       const int rows = i < A.B ? (last[e] - first[e]) * A.G : 0;
-      cls[e] = class_of(rows, many);
+      cls[e] = class_of(r[e].add * A.G, many);  // as the chunk was chosen
       tiles[e] = tiles_of(rows, cls[e]);
-      chunks[e] = max((int)(((int64_t)kv[e] + chunk - 1) / chunk), 1);
+      const int even = even_chunk(kv[e], cls[e] == 2 ? chunk_wide : chunk);
+      chunks[e] = max((kv[e] + even - 1) / even, 1);
       if (chunks[e] > 1) y[0] += tiles[e] * chunks[e] * (rows_of_class(cls[e]) / kUnit);
       if (wg == 0 && i < A.B) {
         A.q_indptr[i] = first[e];
@@ -162,10 +179,6 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
         if (r[e].bad) flags |= LORA_KV_FLAG_LENGTH;
         if (row > A.T || A.add[i] > A.T) flags |= LORA_KV_FLAG_TOKENS;
         if (want > 0 && fresh > A.nfree) flags |= LORA_KV_FLAG_FREE_LIST;
-        // the one cached block that new tokens may lie in
-        if (last[e] > first[e] && (r[e].ctx & (bt - 1)) != 0 &&
-            (unsigned)A.table[i * A.tstride + (r[e].ctx >> A.bt_log2)] >= (unsigned)A.blocks)
-          flags |= LORA_KV_FLAG_BLOCK_RANGE;
       }
     }
     int64_t at2[1], sum2[1], at3[3], sum3[3];
@@ -188,6 +201,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int k = tid * kPer + e;
+      if (last[e] > first[e] && (unsigned)open_block[e] >= (unsigned)A.blocks) flags |= LORA_KV_FLAG_BLOCK_RANGE;
       s_row[k] = first[e];
       s_ctx[k] = r[e].ctx;
       s_kv[k] = kv[e];
@@ -279,6 +293,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       if (tid == kCountMid) v = (int)items0[1];
       if (tid == kCountWide) v = (int)items0[2];
       if (tid == kCountChunk) v = chunk;
+      if (tid == kCountChunkWide) v = chunk_wide;
       if (tid == kCountFlags) v = all;
       if (tid == kCountB) v = A.B;
       if (tid == kCountT) v = A.T;
@@ -295,7 +310,10 @@ hipError_t launch_build(const BuildArgs& A, hipStream_t s) {
   // one work-group per 256 rows or requests, up to 512: each repeats the sums
   // over the requests
   const int grid = min_i(max_i(ceil_div_i(max_i(A.T, A.B), kThreads), 1), 512);
-  build_kernel<<<grid, kThreads, 0, s>>>(A);
+  // one request per thread while a turn of the work-group holds them all: the
+  // serial part of a turn is four times shorter
+  if (A.B <= kThreads) build_kernel<1><<<grid, kThreads, 0, s>>>(A);
+  else build_kernel<4><<<grid, kThreads, 0, s>>>(A);
   return hipGetLastError();
 }
 

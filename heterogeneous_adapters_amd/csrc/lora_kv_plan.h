@@ -13,9 +13,12 @@ constexpr int kChunkStep = 256;  // chunks are multiples of this: a step of each
 constexpr int kMinChunk = 1024;   // smallest chunk of cached tokens per work item
 // Work items (over all kv heads) that the plan aims for.
 constexpr int kTargetItems = 1024;
+// The same for items of 128 rows, two of which fill a compute unit and whose
+// parts cost 64 KB each to join.
+constexpr int kTargetWide = 512;
 
 constexpr int kCountTokens = 0, kCountNewBlocks = 1, kCountItems = 2, kCountParts = 3, kCountChunk = 4,
-              kCountMid = 5, kCountWide = 6, kCountFlags = 8, kCountB = 9, kCountT = 10, kCountCheck = 11,
+              kCountMid = 5, kCountWide = 6, kCountChunkWide = 7, kCountFlags = 8, kCountB = 9, kCountT = 10, kCountCheck = 11,
               kNumCounts = 16;
 
 // Work items by class of their request's rows (new tokens x query heads per
@@ -44,11 +47,27 @@ LORA_KV_HD inline int32_t check_word(int32_t B, int32_t T, int32_t items, int32_
   return (int32_t)(h ^ (h >> 15));
 }
 
+// Tokens per item of a request with kv cached ones: as many items as the
+// step's chunk makes of it, of even length.
+LORA_KV_HD inline int even_chunk(int kv, int chunk) {
+  if (kv <= chunk) return chunk;
+  const int n = (kv + chunk - 1) / chunk, even = (kv + n - 1) / n;
+  return (even + kChunkStep - 1) / kChunkStep * kChunkStep;
+}
+
 // Most work items of a class: sum of tiles_i * ceil(kv_i / chunk) <=
 // sum(tiles_i kv_i) / chunk + sum(tiles_i), the first term at most
 // kTargetItems / hkv by the choice of the chunk, tiles_i <= new_i G / 16 + 1.
 inline int64_t item_cap(int64_t T, int64_t B, int64_t hkv, int64_t G) {
   return kTargetItems / hkv + 1 + T * G / kUnit + 1 + B;
+}
+// The same for one class of a step with T tokens and B requests: its launch's
+// grid (a work-group without an item costs a launch slot: 9.5 us for 5768).
+inline int64_t class_cap(int c, int64_t T, int64_t B, int64_t hkv, int64_t G) {
+  const int64_t split = kTargetItems / hkv + 1;
+  if (c == 0) return T > B ? split + B : item_cap(T, B, hkv, G);
+  if (c == 1) return split + (kMidMost / kMidRows) * B;
+  return split + T * G / kWideRows + B;
 }
 // Room for partial results (16 rows of one chunk each).  A decode step needs
 // at most 2 (kTargetItems / hkv + 1) of them; requests of many rows whose
