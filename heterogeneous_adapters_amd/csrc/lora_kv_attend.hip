@@ -177,6 +177,7 @@ __device__ __forceinline__ bool arrive_last(const AttendArgs& A, const Item& it,
 template <class E, int D, int kThreads>
 __device__ __forceinline__ void join(const AttendArgs& A, const Item& it, int part, int units, int rt, int kvh, float* scratch) {
   constexpr int kVecs = D / 4;
+  constexpr int kBatch = 8;  // chunks in flight per thread
   for (int r = 0; r < rt; ++r) {
     const int live = min(it.nrows - it.row0 - r * kUnit, kUnit);
     if (live <= 0) break;
@@ -189,17 +190,17 @@ __device__ __forceinline__ void join(const AttendArgs& A, const Item& it, int pa
       float M = kNone, L = 0.0f;
       f4 acc{0, 0, 0, 0};
       if (work) {
-        for (int c = groups > 1 ? grp : 0; c < it.chunks; c += 4 * groups) {
-          float2 ml[4], lo[4], hi[4];
+        for (int c = groups > 1 ? grp : 0; c < it.chunks; c += kBatch * groups) {
+          float2 ml[kBatch], lo[kBatch], hi[kBatch];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < kBatch; ++e) {
             const float* p = part_at<D>(A, part + min(c + e * groups, it.chunks - 1) * units + r, kvh);
             ml[e] = get2(p + kUnit * D + 2 * row);
             lo[e] = get2(p + row * D + d);
             hi[e] = get2(p + row * D + d + 2);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < kBatch; ++e) {
             if (c + e * groups >= it.chunks) break;
             const float mn = fmaxf(M, ml[e].x), a = exp2_hw(M - mn), b = exp2_hw(ml[e].x - mn);
             M = mn;

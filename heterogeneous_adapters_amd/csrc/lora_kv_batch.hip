@@ -15,8 +15,6 @@ namespace kv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWavesB = kThreads / 64;
 
 // Inclusive sums over a wave: within rows of 16 lanes, then from row to row.
 template <int CTRL, int ROWS>
@@ -34,7 +32,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
 
 // Exclusive sums of N values over the work-group (32 bits within a wave) and
 // their totals.
-template <int N>
+template <int kWavesB, int N>
 __device__ __forceinline__ void block_scan(const uint32_t (&x)[N], int64_t (&before)[N], int64_t (&total)[N],
                                            uint32_t (*scratch)[8]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -93,9 +91,9 @@ __device__ __forceinline__ int tiles_of(int rows, int cls) {
 }
 
 // kPer: requests per thread and turn.
-template <int kPer>
+template <int kThreads, int kPer>
 __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
-  constexpr int kTurn = kThreads * kPer;
+  constexpr int kTurn = kThreads * kPer, kWavesB = kThreads / 64;
   __shared__ uint32_t s_a[kWavesB][8], s_b[kWavesB][8], s_c[kWavesB][8];
   __shared__ int64_t s_read[2][kWavesB];
   __shared__ int32_t s_row[kTurn];    // first token row
@@ -128,7 +126,9 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   if ((tid & 63) == 0) s_read[0][tid >> 6] = mine, s_read[1][tid >> 6] = mine_wide;
   __syncthreads();
   auto chunk_for = [&](const int64_t* reads, int target) {
-    const int64_t per = ((reads[0] + reads[1] + reads[2] + reads[3]) * A.hkv + target - 1) / target;
+    int64_t sum = 0;
+    for (int w = 0; w < kWavesB; ++w) sum += reads[w];
+    const int64_t per = (sum * A.hkv + target - 1) / target;
     const int64_t rounded = max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)kMinChunk);
     return (int)min(rounded, (int64_t)1 << 29);
   };
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[0] += r[e].add, x[1] += r[e].need - r[e].have;
     int64_t at[2], sum[2];
-    block_scan<2>(x, at, sum, s_a);
+    block_scan<kWavesB, 2>(x, at, sum, s_a);
     // the one cached block of each request that new tokens may lie in
     int open_block[kPer];
 #pragma unroll
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       }
     }
     int64_t at2[1], sum2[1], at3[3], sum3[3];
-    block_scan<1>(y, at2, sum2, s_b);
+    block_scan<kWavesB, 1>(y, at2, sum2, s_b);
     int64_t part = parts0 + at2[0];
     uint32_t z[3] = {0, 0, 0};
 #pragma unroll
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       }
       z[cls[e]] += tiles[e] * chunks[e];
     }
-    block_scan<3>(z, at3, sum3, s_c);
+    block_scan<kWavesB, 3>(z, at3, sum3, s_c);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int k = tid * kPer + e;
@@ -307,13 +307,13 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
 }  // namespace
 
 hipError_t launch_build(const BuildArgs& A, hipStream_t s) {
-  // one work-group per 256 rows or requests, up to 512: each repeats the sums
-  // over the requests
-  const int grid = min_i(max_i(ceil_div_i(max_i(A.T, A.B), kThreads), 1), 512);
-  // one request per thread while a turn of the work-group holds them all: the
-  // serial part of a turn is four times shorter
-  if (A.B <= kThreads) build_kernel<1><<<grid, kThreads, 0, s>>>(A);
-  else build_kernel<4><<<grid, kThreads, 0, s>>>(A);
+  // a work-group per 256 rows or requests, up to 512, each of which repeats
+  // the sums over the requests: in one turn of 256, or turns of 1024, two per
+  // thread (1024 requests: 10.5 us; 256 threads with four each 11.0, 1024 threads
+  // with one each spill, 22)
+  const int grid = min_i(max_i(ceil_div_i(max_i(A.T, A.B), 256), 1), 512);
+  if (A.B <= 256) build_kernel<256, 1><<<grid, 256, 0, s>>>(A);
+  else build_kernel<512, 2><<<ceil_div_i(grid, 2), 512, 0, s>>>(A);
   return hipGetLastError();
 }
 

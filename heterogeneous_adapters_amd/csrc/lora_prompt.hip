@@ -4,8 +4,8 @@
 // sum l of exp2(s - m), s = scale log2(e) q.k.  2 * sum L^2 * heads * D
 // flops: bound by MFMA and, next to it, by the exponentials and LDS reads.
 //
-// bf16: a work-group of kWaves waves takes 32 rows per wave of one query
-// head and walks the prompt's keys in tiles of 64, copied straight into LDS
+// bf16: a work-group of 4 waves takes 32 rows per wave of one query head and
+// walks the prompt's keys in tiles of 32 or 64, copied straight into LDS
 // (buffer loads to LDS, 16 bytes a lane) while the tile before is multiplied.
 // v_mfma_f32_32x32x16_bf16 on both products: S^T = K Q^T leaves row lane%32
 // with tokens 8(i/4) + 4h + i%4 (h = lane/32) in each lane, which is the B
@@ -33,7 +33,13 @@ constexpr float kNone = -1e30f;  // running maximum before any key
 constexpr float kSlack = 8.0f;
 
 constexpr int kRowsPerWave = 32;
-constexpr int kKeys = 64;  // keys per tile
+
+// Keys per tile.  32 halve the scores in flight, which buys a third wave per
+// SIMD at 128 dims and saves registers from spilling to the other bank above
+// (8192 keys at 128 dims: 630 us against 640; 4096 at 192: 126 against 148).
+// Below 128 registers are no bound and 64 keys per barrier win (64 dims, 8192
+// keys: 305 against 331); at 256 either spills and 64 lose less.
+constexpr int keys_per_tile(int D) { return D >= 128 && D < 256 ? 32 : 64; }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -100,8 +106,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* p, i
 #endif
 
 template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
+__global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const PromptArgs A) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kKeys = keys_per_tile(D), kU = kKeys / 32, kC = kKeys / 16;
   constexpr int kRows = W * kRowsPerWave;
   constexpr int kPieces = D / 8;  // 16-byte pieces per row
   constexpr int kTileBytes = kKeys * D * 2;
@@ -176,20 +183,20 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
   float m = kNone, l = 0.0f;
 
   auto compute = [&](int key0, const uint8_t* sk, const uint8_t* sv) {
-    f16v s[2];
+    f16v s[kU];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) {
         const bf16x8 a = *(lds_bf16x8*)(sk + k_at[c % kKVar] + u * 32 * (2 * D) + (c / kKVar) * (kKVar * 32));
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[c], s[u], 0, 0, 0);
       }
 #pragma unroll
-    for (int i = 0; i < kSteps * 2 - 6; ++i) {
+    for (int i = 0; i < kSteps * kU - 6; ++i) {
       if (i == 0) __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -208,14 +215,14 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
     const bool masked = key0 + kKeys - 1 > row_first;
     if (masked) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3) > row) s[u][i] = -INFINITY;
     }
     float most = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) most = fmaxf(most, s[i >> 4][i & 15]);
+    for (int i = 1; i < 16 * kU; ++i) most = fmaxf(most, s[i >> 4][i & 15]);
     most *= A.scale_log2e;
     if (__any(most > m + kSlack)) {
       most = fmaxf(most, __shfl_xor(most, 32));
@@ -225,9 +232,9 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
 #pragma unroll
       for (int d = 0; d < kDims; ++d) o[d] *= alpha;
     }
-    bf16x8 pf[4];
+    bf16x8 pf[kC];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16 * kU; ++i) {
       const float p = exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
       l += p;
       pf[i >> 3][i & 7] = (__bf16)p;
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(const PromptArgs A) {
       return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
     };
 #pragma unroll
-    for (int c = 0; c < 4; ++c)  // 16 tokens each
+    for (int c = 0; c < kC; ++c)  // 16 tokens each
 #pragma unroll
       for (int d = 0; d < kDims; ++d) {
         const s16x8 a = c == 0 ? vf[d] : v_frag(c, d);
