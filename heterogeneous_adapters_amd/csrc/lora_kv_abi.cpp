@@ -236,6 +236,17 @@ static void rotation_geometry(RopeArgs& A, int heads, int dtype) {
   (void)dtype;
 }
 
+// Work-groups of the cache role: 16 rows each, and as many groups of whole
+// passes over the heads as spread a small batch over the chip.
+static int cache_geometry(RopeArgs& A) {
+  const int tiles = ceil_div_i(A.T, 16), at_once = 256 / (16 * A.cache.nc);
+  const int passes = ceil_div_i(A.cache.heads, at_once);
+  const int groups = std::max(1, std::min(passes, ceil_div_i(512, tiles)));
+  A.kv_heads_per_group = ceil_div_i(passes, groups) * at_once;
+  A.kv_groups = ceil_div_i(A.cache.heads, A.kv_heads_per_group);
+  return tiles * A.kv_groups;
+}
+
 lora_status_t lora_rope(const lora_heads_t* q, const lora_heads_t* q_out, const lora_heads_t* k,
                         const lora_heads_t* k_out, const int32_t* positions, int32_t T, int32_t head_dim,
                         int32_t dtype, const lora_rope_t* rope, void* stream) {
@@ -304,12 +315,8 @@ lora_status_t lora_kv_append(const lora_heads_t* q, const lora_heads_t* q_out, c
   A.cache = cache_of(cache);
   A.flags = flags;
   if (A.qo.heads > 0) rotation_geometry(A, A.qo.heads, dtype);
-  const int tiles = ceil_div_i(T, 16), at_once = 256 / (16 * A.cache.nc);
-  const int passes = ceil_div_i(A.cache.heads, at_once);
-  const int groups = std::max(1, std::min(passes, ceil_div_i(512, tiles)));
-  A.kv_heads_per_group = ceil_div_i(passes, groups) * at_once;
-  A.kv_groups = ceil_div_i(A.cache.heads, A.kv_heads_per_group);
-  return hip(launch_rope(A, dtype, A.rot_blocks + tiles * A.kv_groups, static_cast<hipStream_t>(stream)));
+  const int cache_blocks = cache_geometry(A);
+  return hip(launch_rope(A, dtype, A.rot_blocks + cache_blocks, static_cast<hipStream_t>(stream)));
 }
 
 lora_status_t lora_kv_gather(const lora_kv_cache_t* cache, const int32_t* slots, int32_t n, const lora_heads_t* k_out,
@@ -329,8 +336,7 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t* cache, const int32_t* slots,
   A.T = n;
   A.D = cache->head_dim;
   A.cache = cache_of(cache);
-  if ((int64_t)n * A.cache.heads * A.cache.nc / 256 + 1 >= kMaxBlocks) return LORA_ERR_UNSUPPORTED;
-  return hip(launch_gather(A, dtype, static_cast<hipStream_t>(stream)));
+  return hip(launch_gather(A, dtype, cache_geometry(A), static_cast<hipStream_t>(stream)));
 }
 
 size_t lora_kv_workspace_size(const lora_kv_batch_t* b) {

@@ -75,7 +75,7 @@ struct PromptArgs {
 
 hipError_t launch_build(const BuildArgs& A, hipStream_t s);
 hipError_t launch_rope(const RopeArgs& A, int dtype, int blocks, hipStream_t s);
-hipError_t launch_gather(const RopeArgs& A, int dtype, hipStream_t s);
+hipError_t launch_gather(const RopeArgs& A, int dtype, int blocks, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& A, int dtype, bool many, hipStream_t s);
 hipError_t launch_prompt(const PromptArgs& A, int dtype, int D, hipStream_t s);
 

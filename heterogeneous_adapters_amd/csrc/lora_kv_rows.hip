@@ -378,44 +378,101 @@ __global__ __launch_bounds__(kThreads, 4) void rope_kernel(const RopeArgs A) {
 }
 
 // ------------------------------------------------------------------- gather
+// Eight values of four bytes of codes.
+__device__ __forceinline__ void decode8(uint32_t w, float scale, float (&x)[8]) {
+  const uint32_t r[4] = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    x[2 * b] = __uint_as_float(r[b] << 16);
+    x[2 * b + 1] = __uint_as_float(r[b] & 0xffff0000u);
+  }
+}
+
+// The cache role backwards: 16 slots and a share of the heads per work-group.
 template <class E>
 __global__ __launch_bounds__(kThreads) void gather_kernel(const RopeArgs A) {
+  typedef typename E::T T;
+  __shared__ int s_slot[kCacheTokens];
   const Cache& C = A.cache;
   const int nc = C.nc;
-  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t th = idx / nc;
-  const int c = (int)(idx - th * nc);
-  const int64_t t = th / C.heads;
-  const int h = (int)(th - t * C.heads);
-  if (t >= A.T) return;
-  int slot = A.slots[t];
-  if ((unsigned)(slot >> C.bt_log2) >= (unsigned)C.blocks) slot = -1;
-  float k[32], v[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) k[i] = v[i] = 0.0f;
-  if (slot >= 0) {
-    const uint8_t* rec = record(C, slot, h);
-    const int u = slot & 15;
-    const float ks = __uint_as_float((uint32_t)rec[512 * nc + u * nc + c] << 23);
-    const float vs = __uint_as_float((uint32_t)rec[528 * nc + u * nc + c] << 23);
-    auto put = [](float* lo, float* hi, uint32_t byte, float s) {
-      const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(byte, s, 0));
-      *lo = __uint_as_float(w << 16);
-      *hi = __uint_as_float(w & 0xffff0000u);
-    };
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + ((u * 4 + g) * nc + c) * 4);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) put(&k[8 * g + 2 * b], &k[8 * g + 2 * b + 1], w >> (8 * b), ks);
-    }
-    const uint8_t* vc = rec + 256 * nc + (u >> 2) * 64 * nc + 4 * c + (u & 3);
-#pragma unroll
-    for (int d = 0; d < 16; ++d) put(&v[d], &v[16 + d], vc[d * 4 * nc], vs);
+  const int t0 = blockIdx.x / A.kv_groups * kCacheTokens, g = blockIdx.x % A.kv_groups;
+  const int nt = min(kCacheTokens, A.T - t0);
+  const int h_first = g * A.kv_heads_per_group, h_end = min(h_first + A.kv_heads_per_group, C.heads);
+  if (threadIdx.x < kCacheTokens) {
+    int slot = (int)threadIdx.x < nt ? A.slots[t0 + threadIdx.x] : -1;
+    if ((unsigned)(slot >> C.bt_log2) >= (unsigned)C.blocks) slot = -1;
+    s_slot[threadIdx.x] = slot;
   }
-  typedef typename E::T T;
-  store_n<32>(static_cast<T*>(A.ko.p) + t * A.ko.ts + h * A.ko.hs + 32 * c, k);
-  store_n<32>(static_cast<T*>(A.v.p) + t * A.v.ts + h * A.v.hs + 32 * c, v);
+  __syncthreads();
+
+  // K: eight dims per lane
+  {
+    const int per_token = 4 * nc, per_head = nt * per_token, total = (h_end - h_first) * per_head;
+    const Div by_head(per_head), by_token(per_token);
+    for (int idx = threadIdx.x; idx < total; idx += kThreads) {
+      const int hl = by_head(idx), r = idx - hl * per_head, tl = by_token(r), cv = r - tl * per_token;
+      const int slot = s_slot[tl], h = h_first + hl, c = cv >> 2, v = cv & 3, u = slot & 15;
+      float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (slot >= 0) {
+        const uint8_t* rec = record(C, slot, h);
+        const float scale = __uint_as_float((uint32_t)rec[512 * nc + u * nc + c] << 23);
+        decode8(*reinterpret_cast<const uint32_t*>(rec + ((u * 4 + v) * nc + c) * 4), scale, x);
+      }
+      store_n<8>(static_cast<T*>(A.ko.p) + (t0 + tl) * A.ko.ts + h * A.ko.hs + 8 * cv, x);
+    }
+  }
+
+  // V: four lanes hold 4 consecutive slots of one (head, group of 32)
+  const int per_head = kCacheTokens * nc, at_once = kThreads / per_head;
+  const int hl = threadIdx.x / per_head, r = threadIdx.x - hl * per_head;
+  const int j = r & 3, c = (r >> 2) % nc, tl = (r >> 2) / nc * 4 + j, t = t0 + tl;
+  const bool mine = hl < at_once && tl < nt;
+  const int slot = mine ? s_slot[tl] : -1;
+  const int s0 = (int)quad_lane<0>((uint32_t)slot);
+  const uint64_t in_row = __ballot(slot >= 0 && (s0 & 3) == 0 && slot == s0 + j);
+  const bool whole = ((in_row >> (threadIdx.x & 60)) & 15) == 15;
+  const int u = slot & 15;
+  for (int h = h_first + hl; h - hl < h_end; h += at_once) {
+    const bool live = slot >= 0 && h < h_end;
+    const uint8_t* rec = live ? record(C, slot, h) : nullptr;
+    uint32_t q[4] = {0, 0, 0, 0};  // this token's codes: byte k of q[i] is dims 4i+k and 16 more
+    uint32_t d[4] = {0, 0, 0, 0};
+    if (live) {
+      const uint8_t* vc = rec + 256 * nc + (u >> 2) * 64 * nc + 4 * c;
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[k] = *reinterpret_cast<const uint32_t*>(vc + (4 * j + k) * 4 * nc);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i >> 2] |= (uint32_t)vc[i * 4 * nc + (u & 3)] << (8 * (i & 3));
+      }
+    }
+    // of a whole quad lane j read dims 4j..4j+3 of all four tokens: trade
+    const uint32_t lo01 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), hi01 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+    const uint32_t lo23 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u), hi23 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+    const uint32_t of[4] = {__builtin_amdgcn_perm(lo23, lo01, 0x05040100u), __builtin_amdgcn_perm(lo23, lo01, 0x07060302u),
+                            __builtin_amdgcn_perm(hi23, hi01, 0x05040100u), __builtin_amdgcn_perm(hi23, hi01, 0x07060302u)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // token k's word from each lane, for lane k
+      const uint32_t a0 = quad_lane<0>(of[k]), a1 = quad_lane<1>(of[k]), a2 = quad_lane<2>(of[k]), a3 = quad_lane<3>(of[k]);
+      if (whole && k == j) q[0] = a0, q[1] = a1, q[2] = a2, q[3] = a3;
+    }
+    if (mine && h < h_end) {
+      float v[32];
+      const float scale = live ? __uint_as_float((uint32_t)rec[528 * nc + u * nc + c] << 23) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[8];
+        decode8(q[i], scale, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * i + k] = x[2 * k], v[16 + 4 * i + k] = x[2 * k + 1];
+      }
+      store_n<32>(static_cast<T*>(A.v.p) + t * A.v.ts + h * A.v.hs + 32 * c, v);
+    }
+  }
 }
 
 }  // namespace
@@ -432,8 +489,7 @@ hipError_t launch_rope(const RopeArgs& A, int dtype, int blocks, hipStream_t s) 
   return hipGetLastError();
 }
 
-hipError_t launch_gather(const RopeArgs& A, int dtype, hipStream_t s) {
-  const int blocks = ceil_div_i((int64_t)A.T * A.cache.heads * A.cache.nc, kThreads);
+hipError_t launch_gather(const RopeArgs& A, int dtype, int blocks, hipStream_t s) {
   if (dtype == LORA_DTYPE_BF16) gather_kernel<Bf16><<<blocks, kThreads, 0, s>>>(A);
   else gather_kernel<F32><<<blocks, kThreads, 0, s>>>(A);
   return hipGetLastError();
