@@ -164,6 +164,9 @@ lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int3
   if (!block_tokens_ok(block_tokens) || (int64_t)num_blocks * block_tokens > 0x7fffffffll) return LORA_ERR_UNSUPPORTED;
   if (B > batch->max_seqs || T > batch->max_tokens) return LORA_ERR_WORKSPACE;
   const BatchSizes z = batch_sizes(batch->max_tokens, batch->max_seqs, batch->num_q_heads, batch->num_kv_heads);
+  // the call writes the batch while it reads its inputs
+  for (const int32_t* p : {ctx_len, new_len, (const int32_t*)block_table, free_blocks})
+    if (p >= batch->q_indptr && p < batch->q_indptr + z.total / 4) return LORA_ERR_INVALID_ARG;
   BuildArgs A;
   A.ctx = ctx_len;
   A.add = new_len;

@@ -291,7 +291,8 @@ __global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T)
     const int token = (step + W * (lane >> 1)) * kTile + kUnit * (lane & 1);
     int id = 0;
     if (token < end) {
-      id = trow[token >> A.cache.bt_log2];
+      const int at = token >> A.cache.bt_log2;
+      id = at < A.width ? trow[at] : -1;  // a table of another call may be narrower
       if ((unsigned)id >= (unsigned)A.cache.blocks) id = -1, bad_block = true;
     }
     return id;
@@ -516,7 +517,8 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
     const int token = it.begin + (tile + lane) * kKeys + kUnit * wave;
     int id = 0;
     if (token < it.end) {
-      id = trow[token >> A.cache.bt_log2];
+      const int at = token >> A.cache.bt_log2;
+      id = at < A.width ? trow[at] : -1;  // a table of another call may be narrower
       if ((unsigned)id >= (unsigned)A.cache.blocks) id = -1, bad_block = true;
     }
     return id;

@@ -146,7 +146,8 @@ lora_status_t lora_kv_batch_init(void* buf, size_t bytes, int32_t max_tokens, in
  * T: rows of the step's tensors.  Rows behind the last request's (T larger
  * than the sum of new_len: a padded batch) get -1 everywhere and no call
  * touches them.
- * free_blocks may be NULL when num_free is 0.
+ * free_blocks may be NULL when num_free is 0.  No input may lie in the batch's
+ * own buffer (the next step's ctx_len is a copy of kv_len, not kv_len).
  * Errors: INVALID_ARG, WORKSPACE (B or T past the capacity), UNSUPPORTED
  * (block_tokens; num_blocks*block_tokens past 2^31), HIP. */
 lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t T,
@@ -228,9 +229,10 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t* cache, const int32_t* slots,
  * with G = num_q_heads / num_kv_heads.  One new token per request is a
  * decode step; several are a prompt's chunk over its cached context.  A row
  * that sees no token gets zeros; rows that belong to no request are not
- * written.  Tokens in blocks outside the cache are not attended
- * (LORA_KV_FLAG_BLOCK_RANGE in the batch's flags).  B and T must be those of
- * the batch's lora_kv_build, block_table as that call left it.
+ * written.  Tokens in blocks outside the cache, or past the table's width, are
+ * not attended (LORA_KV_FLAG_BLOCK_RANGE in the batch's flags).
+ * B and T must be those of the batch's lora_kv_build, block_table as that call
+ * left it, the cache of the same block_tokens.
  * ws: device, lora_kv_workspace_size(batch) bytes, 16-byte aligned.  The call
  * keeps partial results in ws and arrival counts in the batch's plan, so
  * calls that share either must not run at the same time (issue them on one

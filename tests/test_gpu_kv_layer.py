@@ -196,6 +196,19 @@ def test_blocks_outside_the_cache_are_not_attended():
     assert bool((out[1] == 0).all())  # a row that sees no token
 
 
+@pytest.mark.parametrize("many", [False, True])
+def test_a_cache_of_smaller_blocks_than_the_table_stays_in_the_table(many):
+    """Block tokens of the build and the cache that do not agree: places past the table's width are not read."""
+    s = Step(52, np.array([300, 60]), np.array([40, 1]) if many else np.array([1, 1]), 4, 1, 64, 64, "bf16")
+    s.run(0.125)
+    exact = s.tab[:, :6].contiguous()  # 6 blocks of 64 tokens; the cache below asks for 16-token blocks
+    small = kv.Cache(s.cache.data, 16, 1, 64)
+    out = torch.full_like(s.dq, 5.0)
+    kv.lora_kv_attend(s.dq, out, s.batch, exact.clamp(0, s.num - 1), small, 0.125, s.ws)
+    torch.cuda.synchronize()
+    assert int(s.batch.flags) == kv.FLAG_BLOCK_RANGE
+
+
 def test_a_batch_that_was_not_built_for_the_call_writes_nothing():
     s = Step(51, np.array([10, 20]), np.array([1, 1]), 4, 2, 64, 16, "bf16")
     s.run(0.125)

@@ -127,6 +127,15 @@ def test_build_refusals(kw, code):
     assert kv.lib()["lora_kv_build"](*build_args(Args(), **kw)) == code
 
 
+@pytest.mark.parametrize("which", ["ctx", "new", "table", "free"])
+def test_build_refuses_inputs_in_its_own_batch(which):
+    a = Args()
+    outside = a.p + (1 << 15)
+    # the batch of Args starts at a.p: a copy of it elsewhere leaves the other inputs outside
+    assert kv.lib()["lora_kv_batch_init"](outside, 1 << 30, 64, 8, 8, 2, 64, ctypes.addressof(a.batch)) == 0
+    assert kv.lib()["lora_kv_build"](*build_args(a, **{which: a.batch.kv_len})) == -1
+
+
 @pytest.mark.parametrize("case,code", [
     ("null_q", -1), ("null_pos", -1), ("neg_T", -1), ("dtype", -6), ("dim", -6), ("odd_rot", -1), ("rot_past", -1), ("layout", -6),
     ("null_freq", -1), ("stride", -7), ("short_stride", -1), ("base", -7), ("heads", -1), ("out_missing", -1), ("in_place", -1),
