@@ -81,18 +81,9 @@ __device__ __forceinline__ Span find_span(const PromptArgs& A, int w, int rows) 
 }
 
 // Query head of a launch's b-th work-group among `heads` neighbours.  Work-
-// groups go round the 8 XCDs; where the numbers allow, each XCD gets the
-// query heads of the same kv heads, so that their K and V stay in its L2.
-__device__ __forceinline__ int head_of(int b, int heads, int G) {
-  const int hk_n = heads / G, xcd = b & 7, j = b >> 3;
-  if (heads % 8) return b;
-  if (hk_n % 8 == 0) return (xcd + 8 * (j / G)) * G + j % G;
-  if (8 % hk_n == 0) {
-    const int share = 8 / hk_n;  // XCDs per kv head
-    return xcd / share * G + xcd % share * (heads / 8) + j;
-  }
-  return b;
-}
+// groups go round the 8 XCDs; each XCD gets neighbouring query heads, so that
+// the K and V of their kv heads stay in its L2.
+__device__ __forceinline__ int head_of(int b, int heads) { return heads % 8 ? b : (b & 7) * (heads >> 3) + (b >> 3); }
 
 // Swizzles of 16-byte pieces within a row of D elements, for 64 banks of 4
 // bytes: a K read takes one piece of 16 rows at a time, a V read 4 pieces
@@ -133,7 +124,7 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
   __shared__ __attribute__((aligned(128))) uint8_t s_k0[kTileBytes], s_v0[kTileBytes], s_k1[kTileBytes], s_v1[kTileBytes];
 
   const int hq_n = A.q.heads;
-  const int flat = blockIdx.x / hq_n, hq = head_of(blockIdx.x - flat * hq_n, hq_n, A.G), hk = hq / A.G;
+  const int flat = blockIdx.x / hq_n, hq = head_of(blockIdx.x - flat * hq_n, hq_n), hk = hq / A.G;
   const Span sp = find_span(A, flat, kRows);
   if (sp.tile < 0) return;
 
