@@ -2,7 +2,8 @@
 //
 // Mathematics: per row one pass over the keys with a running maximum m and
 // sum l of exp2(s - m), s = scale log2(e) q.k.  2 * sum L^2 * heads * D
-// flops: bound by MFMA and, next to it, by the exponentials and LDS reads.
+// flops: bound by the issue of products and of the softmax's vector
+// instructions, which share a SIMD's time (56 % and 45 % of it).
 //
 // bf16: a work-group of 4 waves takes 32 rows per wave of one query head and
 // walks the prompt's keys in tiles of 32 or 64, copied straight into LDS
@@ -16,6 +17,12 @@
 // moves.  LDS rows are XOR-swizzled in 16-byte pieces so neither the K reads
 // (eight rows, one piece) nor the V reads (four rows, two pieces) meet in a
 // bank.
+//
+// Measured on MI355X: prompts of 8192, 4097 and 1 tokens, 32 query heads of
+// 128 on 8 kv heads, 610 us = 1.12 PFLOP/s of causal work (the installed
+// library's plain product reaches 1.21); 32 prompts of 128..2048 with 32 kv
+// heads 520 us.  Four waves per work-group: three of them share a CU out of
+// step (8 waves: 683 against 658).
 //
 // fp32 (validation): one wave per 16 rows on v_mfma_f32_16x16x4_f32, keys and
 // values straight from global memory.
