@@ -17,11 +17,14 @@
 // rows are split into three bf16 terms (24 bits), the codes being exact.
 //
 // Measured on MI355X: 128 requests of up to 4097 tokens, 32 kv heads of 128,
-// 257 us = 4.6 TB/s of codes and scales (a copy reaches 4.7): HBM is the
-// bound, with the vector units about half busy converting.  Small steps are
-// bound by latency (one request of 32768 tokens 17 us, 48 of up to 2049 13 us:
-// item, block ids, keys and the join follow one another).  8 waves per work-
-// group rather than 4 halve the partial results per token.
+// 219 us = 5.4 TB/s of codes and scales (a read of 1 GiB reaches 6.1, a copy
+// 4.7): HBM is the bound, with the vector units about half busy converting.
+// The loads of a wave's next step go out, without a branch, before the current
+// one's arithmetic; loads behind a condition, or spilled registers between
+// them (4 waves per SIMD leave 128), cost waits for those just sent: 257 us.
+// Small steps are bound by latency (one request of 32768 tokens 16 us, 48 of
+// up to 2049 12 us: item, block ids, keys and the join follow one another).
+// Work-groups of 4 waves take what those of 8 do, in half the LDS.
 #include <type_traits>
 
 #include "lora_kv_dev.h"
@@ -32,6 +35,7 @@ namespace kv {
 
 namespace {
 
+constexpr int kWaves = 4;  // per work-group of attend_kernel
 constexpr float kNone = -1e30f;  // running maximum before any visible key
 // Rows keep their maximum until a score passes it by this much (a factor of
 // 2^8 in p, without loss: p is scaled the same in the products and the sum).
@@ -49,20 +53,18 @@ __device__ __forceinline__ float2 get2(const float* p) {
 }
 
 template <int NC>
-struct Step {  // one wave's 32 tokens: two units' records
-  uint32_t k[2][NC], v[2][NC];
-  uint8_t ks[2][NC];
-  uint32_t vs[2][NC];
+struct Unit {  // a lane's share of a record
+  uint32_t k[NC], v[NC], ks[(NC + 3) / 4], vs[NC];
 };
 
+// Uniform record, 32-bit lane offsets: scalar base and one offset register.
 template <int NC>
-__device__ __forceinline__ void load_unit(const uint8_t* rec, int lane, uint32_t (&k)[NC], uint32_t (&v)[NC],
-                                          uint8_t (&ks)[NC], uint32_t (&vs)[NC]) {
-  const int m = lane & 15, g = lane >> 4;
-  __builtin_memcpy(k, __builtin_assume_aligned(rec + (m * 4 + g) * 4 * NC, 4), 4 * NC);
-  __builtin_memcpy(v, __builtin_assume_aligned(rec + 256 * NC + (g * 16 + m) * 4 * NC, 4), 4 * NC);
-  __builtin_memcpy(ks, rec + 512 * NC + m * NC, NC);
-  __builtin_memcpy(vs, __builtin_assume_aligned(rec + 528 * NC + 4 * g * NC, 4), 4 * NC);
+__device__ __forceinline__ void load_unit(const uint8_t* rec, int lane, Unit<NC>& x) {
+  const uint32_t m = lane & 15, g = lane >> 4;
+  __builtin_memcpy(x.k, __builtin_assume_aligned(rec + (m * 4 + g) * 4 * NC, 4), 4 * NC);
+  __builtin_memcpy(x.v, __builtin_assume_aligned(rec + 256 * NC + (g * 16 + m) * 4 * NC, 4), 4 * NC);
+  __builtin_memcpy(x.ks, rec + 512 * NC + m * NC, NC);
+  __builtin_memcpy(x.vs, __builtin_assume_aligned(rec + 528 * NC + 4 * g * NC, 4), 4 * NC);
 }
 
 __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float s, int byte) {
@@ -241,10 +243,11 @@ __device__ __forceinline__ void join(const AttendArgs& A, const Item& it, int pa
 }
 
 // RT: tiles of 16 rows per work item.  CLS: the items' class; the fp32 kernel
-// takes the 128 rows of class 2 in four pieces.  W: waves per work-group.
-template <class E, int NC, int RT, int CLS, int W>
-__global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T) == 2 ? 4 : 1) void attend_kernel(const AttendArgs A) {
-  constexpr int kThreads = 64 * W;
+// takes the 128 rows of class 2 in four pieces.  Three waves per SIMD hold two
+// steps' records of a decode step in registers (140 of 168).
+template <class E, int NC, int RT, int CLS>
+__global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename E::T) == 2 ? 3 : 1) void attend_kernel(const AttendArgs A) {
+  constexpr int W = kWaves, kThreads = 64 * W;
   constexpr int NS = sizeof(typename E::T) == 2 ? 1 : 3;
   constexpr int D = 32 * NC, LD = D + 4, kVecs = D / 4;
   constexpr int kPieces = CLS == 2 ? kWideRows / (kUnit * RT) : 1, kUnits = RT * kPieces;
@@ -304,128 +307,128 @@ __global__ __launch_bounds__(64 * W, RT == 1 && NC <= 4 && sizeof(typename E::T)
     }
     return id;
   };
-  auto load_step = [&](Step<NC>& s, int id0, int id1, int step) {
+  int ids = 0, ids_at = -32;  // block ids of steps first + W * (ids_at ..  ids_at + 31)
+  const int mine = (last - first + W - 1) / W;  // this wave's steps
+  // The records of this wave's i-th step.  Past its last step the last one's:
+  // loads without a branch, so that no wait counts on their absence.
+  auto load_step = [&](Unit<NC> (&x)[2], int (&id)[2], int i) {
+    i = min(i, mine - 1);
+    if (i >= ids_at + 32) {
+      ids_at = i;
+      ids = fetch_ids(first + i * W);
+      wait_vm<0>();
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int id = u ? id1 : id0, unit = 2 * step + u;
-      const uint8_t* rec = head + max(id, 0) * A.cache.stride + (unit & unit_mask) * (544 * NC);
-      load_unit<NC>(rec, lane, s.k[u], s.v[u], s.ks[u], s.vs[u]);
+      id[u] = __builtin_amdgcn_readlane(ids, 2 * (i - ids_at) + u);
+      const int unit = 2 * (first + i * W) + u;
+      load_unit<NC>(head + max(id[u], 0) * A.cache.stride + (unit & unit_mask) * (544 * NC), lane, x[u]);
     }
   };
-
-  if (first < last) {
-    int ids = fetch_ids(first);
-    Step<NC> cur, nxt;
-    int id0 = __builtin_amdgcn_readlane(ids, 0), id1 = __builtin_amdgcn_readlane(ids, 1);
-    load_step(cur, id0, id1, first);
-    int k = 0;  // place of the current step among the fetched ids
-    for (int step = first; step < last; step += W) {
-      const int next = step + W;
-      int nid0 = 0, nid1 = 0;
-      if (++k == 32) {
-        k = 0;
-        ids = fetch_ids(next);
-      }
-      if (next < last) {
-        nid0 = __builtin_amdgcn_readlane(ids, 2 * k);
-        nid1 = __builtin_amdgcn_readlane(ids, 2 * k + 1);
-        load_step(nxt, nid0, nid1, next);
-      }
-
-      // S^T = K Q^T
-      f4 s[RT][2];
+  auto compute = [&](Unit<NC> (&cur)[2], const int (&ids2)[2], int step) {
+    const int id0 = ids2[0], id1 = ids2[1];
+    // S^T = K Q^T
+    f4 s[RT][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][u] = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float sc = __uint_as_float((uint32_t)cur.ks[u][c] << 23);
-          const uint32_t w = cur.k[u][c];
-          const bf16x8 a = frag(fp4_pair(w, sc, 0), fp4_pair(w, sc, 1), fp4_pair(w, sc, 2), fp4_pair(w, sc, 3));
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int t = 0; t < NS; ++t) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[r][c][t], s[r][u], 0, 0, 0);
-        }
-      }
-      const int tok = step * kTile;
-      if (tok + kTile > limit0 || id0 < 0 || id1 < 0) {  // some row sees less than the whole step
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int id = u ? id1 : id0, t0 = tok + kUnit * u + 4 * g;
-          uint32_t keep = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-              if (id < 0 || t0 + i >= limit[r]) s[r][u][i] = -INFINITY;
-            if (id >= 0 && t0 + i < end) keep |= 0xffu << (8 * i);
-          }
-          // bytes behind the last token may hold anything, a scale of NaN
-          // among it: 0 * NaN must not reach the products
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            cur.v[u][c] &= keep;
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (!((keep >> (8 * ((4 * c + b) / NC))) & 1)) cur.vs[u][c] &= ~(0xffu << (8 * b));
-          }
-        }
-      }
-
-      bf16x8 pf[RT][NS];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float most = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                           fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * A.scale_log2e;
-        if (__any(most > m[r] + kSlack)) {
-          most = fmaxf(most, __shfl_xor(most, 16));
-          most = fmaxf(most, __shfl_xor(most, 32));
-          const float mn = fmaxf(m[r], most), alpha = exp2_hw(m[r] - mn);
-          m[r] = mn;
-          l[r] *= alpha;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) o[r][c][0] *= alpha, o[r][c][1] *= alpha;
-        }
-        float p[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[i] = exp2_hw(fmaf(s[r][i >> 2][i & 3], A.scale_log2e, -m[r]));
-          l[r] += p[i];
-        }
-        split8<NS>(p, pf[r]);
-      }
-
-      // O^T += V^T P^T
+      for (int r = 0; r < RT; ++r) s[r][u] = f4{0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t r[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int at = j * NC + c;
-            r[j] = fp4_pair(cur.v[u][c], byte_scale(cur.vs[u][at >> 2], at & 3), j);
-          }
-          lo[2 * u] = __builtin_amdgcn_perm(r[1], r[0], 0x05040100u);
-          lo[2 * u + 1] = __builtin_amdgcn_perm(r[3], r[2], 0x05040100u);
-          hi[2 * u] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
-          hi[2 * u + 1] = __builtin_amdgcn_perm(r[3], r[2], 0x07060302u);
-        }
-        const bf16x8 alo = frag(lo[0], lo[1], lo[2], lo[3]), ahi = frag(hi[0], hi[1], hi[2], hi[3]);
+        const float sc = byte_scale(cur[u].ks[c >> 2], c & 3);
+        const uint32_t w = cur[u].k[c];
+        const bf16x8 a = frag(fp4_pair(w, sc, 0), fp4_pair(w, sc, 1), fp4_pair(w, sc, 2), fp4_pair(w, sc, 3));
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int t = 0; t < NS; ++t) {
-            o[r][c][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(alo, pf[r][t], o[r][c][0], 0, 0, 0);
-            o[r][c][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ahi, pf[r][t], o[r][c][1], 0, 0, 0);
-          }
+          for (int t = 0; t < NS; ++t) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[r][c][t], s[r][u], 0, 0, 0);
       }
-      cur = nxt;
-      id0 = nid0;
-      id1 = nid1;
+    }
+    const int tok = step * kTile;
+    if (tok + kTile > limit0 || id0 < 0 || id1 < 0) {  // some row sees less than the whole step
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int id = u ? id1 : id0, t0 = tok + kUnit * u + 4 * g;
+        uint32_t keep = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            if (id < 0 || t0 + i >= limit[r]) s[r][u][i] = -INFINITY;
+          if (id >= 0 && t0 + i < end) keep |= 0xffu << (8 * i);
+        }
+        // bytes behind the last token may hold anything, a scale of NaN
+        // among it: 0 * NaN must not reach the products
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          cur[u].v[c] &= keep;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (!((keep >> (8 * ((4 * c + b) / NC))) & 1)) cur[u].vs[c] &= ~(0xffu << (8 * b));
+        }
+      }
+    }
+
+    bf16x8 pf[RT][NS];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float most = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                         fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * A.scale_log2e;
+      if (__any(most > m[r] + kSlack)) {
+        most = fmaxf(most, __shfl_xor(most, 16));
+        most = fmaxf(most, __shfl_xor(most, 32));
+        const float mn = fmaxf(m[r], most), alpha = exp2_hw(m[r] - mn);
+        m[r] = mn;
+        l[r] *= alpha;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[r][c][0] *= alpha, o[r][c][1] *= alpha;
+      }
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = exp2_hw(fmaf(s[r][i >> 2][i & 3], A.scale_log2e, -m[r]));
+        l[r] += p[i];
+      }
+      split8<NS>(p, pf[r]);
+    }
+
+    // O^T += V^T P^T
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      uint32_t lo[4], hi[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = j * NC + c;
+          r[j] = fp4_pair(cur[u].v[c], byte_scale(cur[u].vs[at >> 2], at & 3), j);
+        }
+        lo[2 * u] = __builtin_amdgcn_perm(r[1], r[0], 0x05040100u);
+        lo[2 * u + 1] = __builtin_amdgcn_perm(r[3], r[2], 0x05040100u);
+        hi[2 * u] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
+        hi[2 * u + 1] = __builtin_amdgcn_perm(r[3], r[2], 0x07060302u);
+      }
+      const bf16x8 alo = frag(lo[0], lo[1], lo[2], lo[3]), ahi = frag(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+          o[r][c][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(alo, pf[r][t], o[r][c][0], 0, 0, 0);
+          o[r][c][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ahi, pf[r][t], o[r][c][1], 0, 0, 0);
+        }
+    }
+  };
+  if (mine > 0) {
+    Unit<NC> one[2], two[2];
+    int id_one[2], id_two[2];
+    load_step(one, id_one, 0);
+    for (int i = 0; i < mine; i += 2) {
+      load_step(two, id_two, i + 1);
+      compute(one, id_one, first + i * W);
+      if (i + 1 >= mine) break;
+      load_step(one, id_one, i + 2);
+      compute(two, id_two, first + (i + 1) * W);
     }
   }
   if (__any(bad_block) && lane == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BLOCK_RANGE);
@@ -532,9 +535,8 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
     }
     return id;
   };
-  uint32_t kc[NC], vc[NC], vs[NC];
-  uint8_t ks[NC];
-  int raw_id = 0;  // block of the unit in kc .. vs
+  Unit<NC> raw;
+  int raw_id = 0;  // its block
   int ids = fetch_ids(0);
   auto load = [&](int tile) {
     if (tile && tile % 64 == 0) ids = fetch_ids(tile);
@@ -542,7 +544,7 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
     const int token = it.begin + tile * kKeys + kUnit * wave;
     // behind the last token: the id is 0, a block of the cache
     const uint8_t* rec = head + max(raw_id, 0) * A.cache.stride + ((token >> 4) & unit_mask) * (544 * NC);
-    load_unit<NC>(rec, lane, kc, vc, ks, vs);
+    load_unit<NC>(rec, lane, raw);
   };
   // The unit in registers to bf16 in LDS.
   auto convert = [&](int tile, auto which) {
@@ -557,23 +559,23 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
         if (raw_id >= 0 && token + 4 * g + i < it.end) keep |= 0xffu << (8 * i);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        vc[c] &= keep;
+        raw.v[c] &= keep;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          if (!((keep >> (8 * ((4 * c + b) / NC))) & 1)) vs[c] &= ~(0xffu << (8 * b));
+          if (!((keep >> (8 * ((4 * c + b) / NC))) & 1)) raw.vs[c] &= ~(0xffu << (8 * b));
       }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const float sc = __uint_as_float((uint32_t)ks[c] << 23);
+      const float sc = byte_scale(raw.ks[c >> 2], c & 3);
       const int t = kUnit * wave + m16;
       *reinterpret_cast<u32x4*>(s_k[buf] + t * (2 * D) + swz_k(t, 4 * c + g) * 16) =
-          u32x4{fp4_pair(kc[c], sc, 0), fp4_pair(kc[c], sc, 1), fp4_pair(kc[c], sc, 2), fp4_pair(kc[c], sc, 3)};
+          u32x4{fp4_pair(raw.k[c], sc, 0), fp4_pair(raw.k[c], sc, 1), fp4_pair(raw.k[c], sc, 2), fp4_pair(raw.k[c], sc, 3)};
       uint32_t r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int at = j * NC + c;
-        r[j] = fp4_pair(vc[c], byte_scale(vs[at >> 2], at & 3), j);
+        r[j] = fp4_pair(raw.v[c], byte_scale(raw.vs[at >> 2], at & 3), j);
       }
       // tokens 4g..4g+3 of the unit, one dim: 8 bytes; the two halves of a
       // 16-byte piece are the tokens 8 apart that one lane of P holds
@@ -710,15 +712,13 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
 
 template <class E, int NC>
 hipError_t launch(const AttendArgs& A, bool many, hipStream_t s) {
-  // 8 waves join through 64 KB of LDS at 128 dims; past that, 4
-  constexpr int W = NC <= 4 ? 8 : 4;
   auto blocks = [&](int c) { return (unsigned)(class_cap(c, A.T, A.B, A.cache.heads, A.G) * A.cache.heads); };
   if (many) {
     if constexpr (sizeof(typename E::T) == 2) attend_wide_kernel<NC><<<blocks(2), 256, 0, s>>>(A);
-    else attend_kernel<E, NC, 2, 2, W><<<blocks(2) * (kWideRows / kMidRows), 64 * W, 0, s>>>(A);
-    attend_kernel<E, NC, 2, 1, W><<<blocks(1), 64 * W, 0, s>>>(A);
+    else attend_kernel<E, NC, 2, 2><<<blocks(2) * (kWideRows / kMidRows), 64 * kWaves, 0, s>>>(A);
+    attend_kernel<E, NC, 2, 1><<<blocks(1), 64 * kWaves, 0, s>>>(A);
   }
-  attend_kernel<E, NC, 1, 0, W><<<blocks(0), 64 * W, 0, s>>>(A);
+  attend_kernel<E, NC, 1, 0><<<blocks(0), 64 * kWaves, 0, s>>>(A);
   return hipGetLastError();
 }
 

@@ -9,7 +9,7 @@ namespace kv {
 
 constexpr int kUnit = 16;        // tokens per cache record, rows per attention tile
 constexpr int kTile = 32;        // cached tokens per step of a wave
-constexpr int kChunkStep = 256;  // chunks are multiples of this: a step of each of 8 waves
+constexpr int kChunkStep = 256;  // chunks are multiples of this: two steps of each of 4 waves
 constexpr int kMinChunk = 1024;   // smallest chunk of cached tokens per work item
 // Work items (over all kv heads) that the plan aims for.
 constexpr int kTargetItems = 1024;
