@@ -17,7 +17,7 @@
 // rows are split into three bf16 terms (24 bits), the codes being exact.
 //
 // Measured on MI355X: 128 requests of up to 4097 tokens, 32 kv heads of 128,
-// 219 us = 5.4 TB/s of codes and scales (a read of 1 GiB reaches 6.1, a copy
+// 213 us = 5.5 TB/s of codes and scales (a read of 1 GiB reaches 6.1, a copy
 // 4.7): HBM is the bound, with the vector units about half busy converting.
 // The loads of a wave's next step go out, without a branch, before the current
 // one's arithmetic; loads behind a condition, or spilled registers between
@@ -483,9 +483,10 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename 
 // 16 tokens by each wave, into LDS, while the tile before is multiplied with
 // v_mfma_f32_32x32x16_bf16, 32 rows per wave.  K lies by token, V by dim in the
 // token order of P's registers, both XOR-swizzled in 16-byte pieces against
-// the 64 banks.  Four chunks of 512 tokens over 5000, 32 query heads: 220 to
-// 260 us, 600-700 TFLOP/s (16 rows at a time: 500; 32 rows without LDS: 292),
-// bound by the issue of conversions, exponentials and products.
+// the 64 banks.  Four chunks of 512 tokens over 5000, 32 query heads: 213 to
+// 224 us, 680-710 TFLOP/s (16 rows at a time: 500 us; 32 rows without LDS:
+// 292), bound by the issue of conversions and exponentials (48 % of the time)
+// and products (41 %).
 template <int NC>
 __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A) {
   constexpr int D = 32 * NC, kThreads = 256, kKeys = 64, kUnits = kWideRows / kUnit;
