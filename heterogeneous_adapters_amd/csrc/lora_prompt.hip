@@ -23,9 +23,10 @@
 // step (8 waves: 683 against 658).
 //
 // fp32 (validation): one wave per 16 rows on v_mfma_f32_16x16x4_f32, keys and
-// values straight from global memory, a step's all loaded before its products:
-// bound by the L2 that every wave reads them from (32 prompts of up to 400, 32
-// heads of 128 on 8: 272 us, 52 TFLOP/s; each value loaded where it is used, 748).
+// values straight from global memory, a step's all loaded before its products
+// (32 prompts of up to 400, 32 heads of 128 on 8: 272 us, 52 TFLOP/s; each value
+// loaded where it is used, 748).  Short prompts are bound by the chain of
+// products of their last rows, long ones by every wave's reads of the caches.
 #include "lora_kv_dev.h"
 #include "lora_kv_host.h"
 
