@@ -13,8 +13,11 @@
 // v_cvt_scalef32_pk_bf16_fp4 (exact), and multiplies on
 // v_mfma_f32_16x16x32_bf16: S^T = K Q^T, whose result layout (row = lane%16,
 // tokens 4g..4g+3 of each 16) is the B operand that O^T = V^T P^T needs, with
-// the record's V order supplying A, so P never leaves its registers.  fp32
-// rows are split into three bf16 terms (24 bits), the codes being exact.
+// the record's V order supplying A, so P never leaves its registers.  It is
+// rounded to bf16 there, by up to 2^-8 of each weight (a second term would
+// double the second product); l sums the rounded weights, so that they sum to
+// one (no change in time).  fp32 rows and weights are split into three bf16
+// terms (24 bits), the codes being exact.
 //
 // Measured on MI355X: 128 requests of up to 4097 tokens, 32 kv heads of 128,
 // 213 us = 5.5 TB/s of codes and scales (a read of 1 GiB reaches 6.1, a copy
@@ -387,9 +390,10 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename 
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         p[i] = exp2_hw(fmaf(s[r][i >> 2][i & 3], A.scale_log2e, -m[r]));
-        l[r] += p[i];
+        if (NS > 1) l[r] += p[i];
       }
       split8<NS>(p, pf[r]);
+      if (NS == 1) l[r] = add8(pf[r][0], l[r]);
     }
 
     // O^T += V^T P^T
@@ -654,9 +658,7 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
     bf16x8 pf[4];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const float p = exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
-      l += p;
-      pf[i >> 3][i & 7] = (__bf16)p;
+      pf[i >> 3][i & 7] = (__bf16)exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -664,6 +666,7 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
       for (int d = 0; d < kDims; ++d) {
         const bf16x8 a = *reinterpret_cast<const bf16x8*>(sv + v_at[c] + d * (32 * 2 * kKeys));
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pf[c], o[d], 0, 0, 0);
+        if (d == 0) l = add8(pf[c], l);
       }
   };
 

@@ -28,6 +28,16 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// l plus the eight values of f: two per instruction, summed in fp32 (checked on
+// gfx950: within 0.69 units in the last place, nearest in all but 20 of 65536
+// draws).
+__device__ __forceinline__ float add8(bf16x8 f, float l) {
+  const bf16x2 one{(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{f[i], f[i + 1]}, one, l, false);
+  return l;
+}
+
 // Element types: vectors of 16 bytes to and from fp32.
 struct Bf16 {
   typedef uint16_t T;

@@ -20,7 +20,11 @@
  *
  * Element types: LORA_DTYPE_BF16 (q, k, v and outputs bf16) or
  * LORA_DTYPE_F32.  Scores, softmax statistics and every accumulation are
- * fp32.
+ * fp32.  With bf16 each softmax weight is rounded to bf16 (by at most 2^-8 of
+ * it) for its product with V, as the bf16 matrix instructions take it; the sum
+ * that divides the result is of the rounded weights, so that the weights sum
+ * to one (rows that see one and the same V return it).  With fp32 weights
+ * keep 24 bits.
  */
 #ifndef LORA_KV_H
 #define LORA_KV_H
