@@ -39,10 +39,6 @@ namespace kv {
 namespace {
 
 constexpr int kWaves = 4;  // per work-group of attend_kernel
-constexpr float kNone = -1e30f;  // running maximum before any visible key
-// Rows keep their maximum until a score passes it by this much (a factor of
-// 2^8 in p, without loss: p is scaled the same in the products and the sum).
-constexpr float kSlack = 8.0f;
 
 // Partial results cross XCDs within the launch: agent-scope accesses (write
 // through, and past the reader's own L2), 8 bytes each, no cache maintenance.
@@ -285,6 +281,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename 
 
   f4 o[RT][NC][2];
   float m[RT], l[RT];
+  bool far = false;  // some row's scores are
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     m[r] = kNone;
@@ -382,14 +379,21 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename 
         most = fmaxf(most, __shfl_xor(most, 32));
         const float mn = fmaxf(m[r], most), alpha = exp2_hw(m[r] - mn);
         m[r] = mn;
+        far = far || __any(is_far(mn));
         l[r] *= alpha;
 #pragma unroll
         for (int c = 0; c < NC; ++c) o[r][c][0] *= alpha, o[r][c][1] *= alpha;
       }
+      float scale = A.scale_log2e, less = m[r];
+      if (far) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[r][i >> 2][i & 3] = far_exponent(s[r][i >> 2][i & 3], scale, less);
+        scale = 1.0f, less = 0.0f;
+      }
       float p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = exp2_hw(fmaf(s[r][i >> 2][i & 3], A.scale_log2e, -m[r]));
+        p[i] = exp2_hw(fmaf(s[r][i >> 2][i & 3], scale, -less));
         if (NS > 1) l[r] += p[i];
       }
       split8<NS>(p, pf[r]);
@@ -607,6 +611,7 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = kNone, l = 0.0f;
+  bool far = false;  // some row's scores are
 
   auto compute = [&](int tile, auto which) {
     constexpr int buf = which;
@@ -651,15 +656,20 @@ __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A)
       most = fmaxf(most, __shfl_xor(most, 32));
       const float mn = fmaxf(m, most), alpha = exp2_hw(m - mn);
       m = mn;
+      far = far || __any(is_far(mn));
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < kDims; ++d) o[d] *= alpha;
     }
+    float scale = A.scale_log2e, less = m;
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = far_exponent(s[i >> 4][i & 15], scale, less);
+      scale = 1.0f, less = 0.0f;
+    }
     bf16x8 pf[4];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      pf[i >> 3][i & 7] = (__bf16)exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
-    }
+    for (int i = 0; i < 32; ++i) pf[i >> 3][i & 7] = (__bf16)exp2_hw(fmaf(s[i >> 4][i & 15], scale, -less));
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll

@@ -38,6 +38,24 @@ __device__ __forceinline__ float add8(bf16x8 f, float l) {
   return l;
 }
 
+// Running maximum before any visible key: the lowest finite number, which no
+// score in range is below.
+constexpr float kNone = -3.402823466e38f;
+// Rows keep their maximum until a score passes it by this much (a factor of
+// 2^8 in p, without loss: p is scaled the same in the products and the sum).
+constexpr float kSlack = 8.0f;
+// p = exp2(s scale - m) is one fma from the exact product, while m is a rounded
+// one: a factor common to the row, of up to 2^64 while m is below 2^30.  Past
+// that it would leave fp32's range, so there the product is rounded as m was,
+// and p of the largest score is 1.
+constexpr float kFar = 1073741824.0f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && m != kNone; }
+__device__ __forceinline__ float far_exponent(float s, float scale, float m) {
+#pragma clang fp contract(off)
+  const float product = s * scale;
+  return product - m;
+}
+
 // Element types: vectors of 16 bytes to and from fp32.
 struct Bf16 {
   typedef uint16_t T;

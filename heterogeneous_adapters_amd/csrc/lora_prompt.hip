@@ -41,11 +41,6 @@ namespace kv {
 
 namespace {
 
-constexpr float kNone = -1e30f;  // running maximum before any key
-// Rows keep their maximum until a score passes it by this much (a factor of
-// 2^8 in p, without loss: p is scaled the same in the products and the sum).
-constexpr float kSlack = 8.0f;
-
 constexpr int kRowsPerWave = 32;
 
 // Keys per tile.  32 halve the scores in flight, which buys a third wave per
@@ -253,9 +248,7 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
     }
     bf16x8 pf[kC];
 #pragma unroll
-    for (int i = 0; i < 16 * kU; ++i) {
-      pf[i >> 3][i & 7] = (__bf16)exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
-    }
+    for (int i = 0; i < 16 * kU; ++i) pf[i >> 3][i & 7] = (__bf16)exp2_hw(fmaf(s[i >> 4][i & 15], A.scale_log2e, -m));
     // O^T += V^T P^T
     auto v_frag = [&](int c, int d) {
       s16x4 part[2];
@@ -292,7 +285,9 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
   }
 
   // A weight of zero does not hide an infinity or NaN of V from the product:
-  // rows that are not finite are computed again, key by key visible or not.
+  // rows that are not finite are computed again, key by key visible or not, and
+  // so are rows of far scores, whose form of the weights would cost the loop
+  // above registers.
   float odd = 0.0f;  // stays 0 while all is finite
   auto write = [&](float inv, bool check) {
     uint16_t* out = static_cast<uint16_t*>(A.o.p) + (int64_t)(sp.begin + row) * A.o.ts + hq * A.o.hs;
@@ -312,7 +307,7 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
   };
   l += __shfl_xor(l, 32);
   if (row <= row_last) write(1.0f / l, true);
-  if (!__any(odd != odd)) return;
+  if (!__any(odd != odd || is_far(m))) return;
 
   // The long way, straight from global memory, 32 keys a step: the finite part
   // of V as usual, then, for each sign and for NaN, a product that counts the
@@ -352,7 +347,7 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
       bf16x8 p, sees;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        p[j] = (__bf16)exp2_hw(fmaf(s[8 * c + j], A.scale_log2e, -m));
+        p[j] = (__bf16)exp2_hw(far_exponent(s[8 * c + j], A.scale_log2e, m));
         sees[j] = key0 + 16 * c + 8 * (j >> 2) + 4 * h + (j & 3) <= row ? (__bf16)1.0f : (__bf16)0.0f;
       }
       l = add8(p, l);
@@ -422,6 +417,7 @@ __global__ __launch_bounds__(256) void prompt_f32_kernel(const PromptArgs A) {
     o[s] = f4{0, 0, 0, 0};
   }
   float m = kNone, l = 0.0f;
+  bool far = false;  // some row's scores are
   f4 k[kVecs];
   auto load_k = [&](int key0) {
     const float* kr = kb + (int64_t)min(key0 + n, sp.len - 1) * A.k.ts + 4 * g;
@@ -455,6 +451,7 @@ __global__ __launch_bounds__(256) void prompt_f32_kernel(const PromptArgs A) {
       most = fmaxf(most, __shfl_xor(most, 32));
       const float mn = fmaxf(m, most), alpha = exp2_hw(m - mn);
       m = mn;
+      far = far || __any(is_far(mn));
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < kVecs; ++d) o[d] *= alpha;
@@ -462,7 +459,7 @@ __global__ __launch_bounds__(256) void prompt_f32_kernel(const PromptArgs A) {
     float p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      p[i] = exp2_hw(fmaf(s[i], A.scale_log2e, -m));
+      p[i] = exp2_hw(far ? far_exponent(s[i], A.scale_log2e, m) : fmaf(s[i], A.scale_log2e, -m));
       l += p[i];
     }
     if (masked) {

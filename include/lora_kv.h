@@ -24,7 +24,8 @@
  * it) for its product with V, as the bf16 matrix instructions take it; the sum
  * that divides the result is of the rounded weights, so that the weights sum
  * to one (rows that see one and the same V return it).  With fp32 weights
- * keep 24 bits.
+ * keep 24 bits.  Scores may be of any size, as long as scale * log2(e) * q.K
+ * stays within fp32's range.
  */
 #ifndef LORA_KV_H
 #define LORA_KV_H

@@ -1,11 +1,12 @@
-"""The attention operators over the rest of their range: weights that sum to one."""
+"""The attention operators over the rest of their range: weights that sum to
+one, scores far from zero."""
 import math
 
 import numpy as np
 import pytest
 
 import kv_reference as R
-from test_gpu_kv import Step
+from test_gpu_kv import Step, normal
 from test_gpu_prompt import run_prompt
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +79,87 @@ def test_cache_weights_sum_to_one(ctx, new, hq, hkv, D, bt):
     put_step(s, star(s.T, hq, 1, D)[0], k, v)
     got = s.run(math.log(2.0))
     assert np.array_equal(got, np.broadcast_to(v, got.shape))
+
+
+# ------------------------------------------------------- scores far from zero
+# Scores of +-2^60 and beyond, up to the end of fp32: q has one dim that is not
+# zero, so that every score is one exact product.  At these sizes the weights
+# are 1 for the largest score and 0 for every lower one (steps of a factor of
+# 1.5), so a row is the mean of V over the keys that share the largest score:
+# sums of at most n equal weights, one reciprocal and one product, (n + 4)
+# roundings of 2^-24 of the mean of |V|, and one rounding of the result.
+FAR = [(30, 1), (31, -1), (33, 1), (47, -1), (60, 1), (106, -1), (106, 1), (124, -1), (124, 1)]
+
+
+def far_rows(level, v, sees, G):
+    """Mean of V over the keys of the highest level, and the mean of |V|.  level (L,), v (L, hkv, D)."""
+    o, a = (np.zeros((len(sees), v.shape[1] * G, v.shape[2])) for _ in range(2))
+    for j, n in enumerate(sees):
+        best = level[:n] == level[:n].max()
+        o[j], a[j] = np.repeat(v[:n][best].mean(0), G, axis=0), np.repeat(np.abs(v[:n][best]).mean(0), G, axis=0)
+    return o, a
+
+
+def far_check(got, o, a, n, dtype):
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    bad = ~(np.abs(got - o) <= half * np.abs(o) + (n + 4) * 2.0 ** -24 * a * (1 + half))
+    assert not bad.any(), np.argwhere(bad)[:5]
+
+
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+@pytest.mark.parametrize("power,sign", FAR)
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_prompt_scores_far_from_zero(dtype, D, power, sign, order):
+    rng = np.random.default_rng(power)
+    T, hq, hkv = 150, 2, 1
+    c = rng.choice([1.0, 1.5, 2.0, 3.0], T)
+    if order != "mixed":
+        c = np.sort(c)[:: 1 if order == "up" else -1]
+    q, k = np.zeros((T, hq, D)), np.zeros((T, hkv, D))
+    q[..., 0] = sign * 2.0 ** (power // 2)
+    k[..., 0] = c[:, None] * 2.0 ** (power - power // 2)
+    v = normal(rng, (T, hkv, D), dtype)
+    got = run_prompt(q, k, v, [0, T], 1.0, dtype)
+    o, a = far_rows(sign * c, v, np.arange(1, T + 1), hq // hkv)
+    far_check(got, o, a, T, dtype)
+
+
+@pytest.mark.parametrize("power,sign", FAR)
+@pytest.mark.parametrize("ctx,new,D,dtype", [([0, 2100, 40], [1, 1, 1], 64, "bf16"), ([70, 2], [30, 1], 128, "bf16"),
+                                             ([1200, 0], [90, 1], 64, "bf16"), ([30, 0], [70, 1], 256, "bf16"),
+                                             ([0, 1100], [1, 1], 64, "f32"), ([60], [50], 96, "f32")])
+def test_cache_scores_far_from_zero(ctx, new, D, dtype, power, sign):
+    s = Step(70 + D, np.array(ctx), np.array(new), 2, 1, D, 16, dtype)
+    level = s.rng.choice([1.0, 1.5, 2.0, 3.0], len(s.k))
+    k = np.zeros_like(s.k)
+    k[..., 0] = level[:, None] * 2.0 ** (power - power // 2)
+    q = np.zeros_like(s.q)
+    q[..., 0] = sign * 2.0 ** (power // 2)
+    put_step(s, q, k, s.v)
+    got = s.run(1.0)
+    for i, rows, at, L in s.rows():
+        o, a = far_rows(sign * level[at:at + L], s.v[at:at + L], s.ctx[i] + np.arange(rows.stop - rows.start) + 1, 2)
+        far_check(got[rows], o, a, L, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_with_ordinary_and_far_scores_side_by_side(dtype):
+    """Query heads of one tile: one with scores of 2^100, one of ordinary size, one that is all zeros."""
+    D, T = 64, 100
+    rng = np.random.default_rng(2)
+    q, k, v = normal(rng, (T, 3, D), dtype), normal(rng, (T, 1, D), dtype), normal(rng, (T, 1, D), dtype)
+    q[:, 2] = 0.0
+    far = q.copy()
+    far[:, 0] *= 2.0 ** 100
+    scale = 1.0 / math.sqrt(D)
+    got, want = run_prompt(far, k, v, [0, T], scale, dtype), run_prompt(q, k, v, [0, T], scale, dtype)
+    assert np.array_equal(got[:, 1:], want[:, 1:]) and np.isfinite(got).all()
+    s = Step(90, np.array([90]), np.array([5]), 3, 1, D, 16, dtype)
+    plain = s.run(scale)
+    s.q[:, 0] *= 2.0 ** 100
+    mixed = s.run(scale)
+    # a tile's rows share the form of their weights, which differs by one rounding of the score
+    o, a, s_abs = R.attend_rows(s.q[:, 1:], np.repeat(s.k, 2, 1), np.repeat(s.v, 2, 1), 91 + np.arange(5), scale)
+    extra = 2.0 ** -8 * np.abs(o) if dtype == "bf16" else 0.0  # the sum is of rounded weights too
+    assert np.all(np.abs(mixed[:, 1:] - o) <= R.attend_bound(o, a, s_abs, 95, D, dtype) + extra)
+    assert np.isfinite(mixed).all() and np.isfinite(plain).all()
