@@ -7,8 +7,9 @@
 //          where fp32 would have lost the angle.  cos and sin of it in fp64,
 //          once per (token, pair), shared by the heads of a work-group
 //          through LDS.
-//   K      rotated in fp64 and rounded once; Q in fp32 from the rounded cos
-//          and sin (its 2^-24 disappears in the rounding to bf16).
+//   K      rotated in fp64 and rounded once; Q too where it is fp32, while bf16
+//          Q is rotated in fp32 from the rounded cos and sin (2^-24, which
+//          disappears in the rounding to bf16).
 //   codes  2^e = the smallest power of two with max|x| <= 7 * 2^e, read off
 //          the bits of max|x|: fraction above 1.75 moves to the next power.
 //          v_cvt_scalef32_pk_fp4_f32 divides by 2^e, rounds to nearest even
@@ -153,6 +154,7 @@ __device__ __forceinline__ void rotate_heads(const RopeArgs& A, const Rows& in, 
 
 template <class E>
 __device__ __forceinline__ void rotate_role(const RopeArgs& A, int block, double2* lds) {
+  constexpr bool kBf16 = sizeof(typename E::T) == 2;
   float2* lf = reinterpret_cast<float2*>(lds + kRotTokens * kMaxPairs);
   const int half = A.rot >> 1;
   const int t0 = block / A.q_groups * kRotTokens, g = block % A.q_groups;
@@ -163,14 +165,18 @@ __device__ __forceinline__ void rotate_role(const RopeArgs& A, int block, double
       if (p < 0) continue;
       const double2 w = angle(A, p, i - tl * half);
       lds[i] = w;
-      lf[i] = make_float2((float)w.x, (float)w.y);
+      if constexpr (kBf16) lf[i] = make_float2((float)w.x, (float)w.y);
     }
     __syncthreads();
   };
   // heads of q, then of k
   const int lo = g * A.q_heads_per_group, hi = min(lo + A.q_heads_per_group, A.qo.heads + A.ko.heads);
   const int nq = min(hi, A.qo.heads) - min(lo, A.qo.heads), nk = hi - lo - nq;
-  if (nq > 0) rotate_heads<E, float>(A, A.q, A.qo, t0, nt, lo, nq, lf, angles);
+  if constexpr (kBf16) {
+    if (nq > 0) rotate_heads<E, float>(A, A.q, A.qo, t0, nt, lo, nq, lf, angles);
+  } else {
+    if (nq > 0) rotate_heads<E, double>(A, A.q, A.qo, t0, nt, lo, nq, lds, angles);
+  }
   if (nk > 0) {
     const int h0 = max(lo - A.qo.heads, 0);
     if (nq > 0) rotate_heads<E, double>(A, A.k, A.ko, t0, nt, h0, nk, lds, [] {});

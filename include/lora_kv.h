@@ -167,8 +167,8 @@ lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int3
  * with f_i = inv_freq[i] (device, rot_dim/2 doubles, radians per position).
  * Dims from rot_dim on are passed through.  Angles are reduced in 64 bits,
  * whatever the position; K is rotated in 64 bits and rounded once, so that
- * the codes of lora_kv_append do not depend on how a product was summed; Q in
- * fp32. */
+ * the codes of lora_kv_append do not depend on how a product was summed; fp32
+ * Q likewise, bf16 Q in fp32 before its one rounding. */
 #define LORA_ROPE_HALF 0
 #define LORA_ROPE_INTERLEAVED 1
 typedef struct {

@@ -1,12 +1,14 @@
 """The attention operators over the rest of their range: weights that sum to
-one, scores far from zero."""
+one, scores far from zero, fp32 queries rotated in 64 bits."""
 import math
 
 import numpy as np
 import pytest
+import torch
 
 import kv_reference as R
-from test_gpu_kv import Step, normal
+from heterogeneous_adapters_amd import kv
+from test_gpu_kv import DEV, Step, host, i32, normal, to_dev
 from test_gpu_prompt import run_prompt
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +165,27 @@ def test_rows_with_ordinary_and_far_scores_side_by_side(dtype):
     extra = 2.0 ** -8 * np.abs(o) if dtype == "bf16" else 0.0  # the sum is of rounded weights too
     assert np.all(np.abs(mixed[:, 1:] - o) <= R.attend_bound(o, a, s_abs, 95, D, dtype) + extra)
     assert np.isfinite(mixed).all() and np.isfinite(plain).all()
+
+
+# ---------------------------------------------------------- rotation in 64 bits
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,hq,hk,D,rot", [(9, 8, 2, 128, 128), (5, 3, 0, 64, 20), (17, 4, 4, 256, 128), (1, 1, 1, 32, 32)])
+def test_fp32_queries_are_rotated_in_64_bits_and_rounded_once(T, hq, hk, D, rot, interleaved):
+    rng = np.random.default_rng(T + D)
+    q, k, v = (normal(rng, (T, max(h, 1), D), "f32") for h in (hq, hk, hk))
+    pos = rng.integers(0, 1 << 16, T)
+    freq, scale = R.frequencies(rot, 10000.0, "yarn", 8.0, 4096)
+    rope = kv.Rope(torch.tensor(freq, dtype=torch.float64, device=DEV), int(interleaved), scale)
+    want = R.round_to(R.rotate(q, pos, freq, scale, interleaved), "f32")
+    dq, outs = to_dev(q, "f32"), []
+    outs.append(torch.zeros_like(dq))
+    kv.lora_rope(dq, outs[0], to_dev(k, "f32") if hk else None, to_dev(k, "f32") if hk else None, i32(pos), rope)
+    data = torch.zeros((T, R.block_bytes(16, k.shape[1], D)), dtype=torch.uint8, device=DEV)
+    outs.append(torch.zeros_like(dq))
+    kv.lora_kv_append(dq, outs[1], to_dev(k, "f32"), to_dev(v, "f32"), i32(pos), i32(np.arange(T) * 16), rope, kv.Cache(data, 16, k.shape[1], D))
+    torch.cuda.synchronize()
+    for got in outs:
+        # the same but for values next to a border: the plain form's angles are off by up to 2^-53 * 2^16 radians
+        # (a turn rounded to 53 bits), 2^-13 of half a step
+        got = host(got)
+        assert np.all(np.abs(got - want) <= 2 * 2.0 ** -24 * np.abs(want)) and np.mean(got != want) < 1e-3
