@@ -121,6 +121,16 @@ def _ints(t: torch.Tensor, name: str, dim: int = 1) -> int:
     return t.data_ptr()
 
 
+def _table(t: torch.Tensor):
+    """(address, row stride, width) of a block table."""
+    at, (rows, width), stride = _ints(t, "block_table", 2), t.shape, t.stride(0)
+    if stride < width:
+        if rows > 1:
+            raise ValueError(f"block_table's rows overlap: {stride} entries apart, {width} wide")
+        stride = width
+    return at, stride, width
+
+
 def _call(name: str, stream, tensors, *args) -> None:
     """The C call on the tensors' device and its current stream (or `stream`)."""
     dev = tensors[0].get_device()
@@ -250,13 +260,12 @@ def lora_kv_build(ctx_len: torch.Tensor, new_len: torch.Tensor, T: int, block_ta
                   free_blocks: torch.Tensor, num_blocks: int, block_tokens: int, batch: Batch, stream=None) -> None:
     """Rows, positions, slots and plan of a step from request lengths; new
     blocks go from free_blocks into block_table (B, width)."""
-    B, width = ctx_len.shape[0], block_table.shape[-1]
+    (table, stride, width), B = _table(block_table), ctx_len.shape[0]
     if new_len.shape[0] != B or block_table.shape[0] != B:
         raise ValueError("one length of each kind and one table row per request")
     _call("lora_kv_build", stream, (ctx_len, new_len, block_table, free_blocks, batch.buf),
-          _ints(ctx_len, "ctx_len"), _ints(new_len, "new_len"), B, T, _ints(block_table, "block_table", 2),
-          max(block_table.stride(0), width), width, _ints(free_blocks, "free_blocks"), free_blocks.shape[0], num_blocks,
-          block_tokens, batch.ref)
+          _ints(ctx_len, "ctx_len"), _ints(new_len, "new_len"), B, T, table, stride, width, _ints(free_blocks, "free_blocks"),
+          free_blocks.shape[0], num_blocks, block_tokens, batch.ref)
     if batch.T != T or batch.B != B:
         batch._resize(T, B)
 
@@ -321,12 +330,12 @@ def lora_kv_gather(cache: Cache, slots: torch.Tensor, k_out: torch.Tensor, v_out
 def lora_kv_attend(q: torch.Tensor, out: torch.Tensor, batch: Batch, block_table: torch.Tensor, cache: Cache,
                    scale: float, ws: torch.Tensor, stream=None) -> None:
     """Attention of the batch's rows q (T, heads, head_dim) over the cache."""
-    table, width, dtype = _ints(block_table, "block_table", 2), block_table.shape[1], q.dtype
+    (table, stride, width), dtype = _table(block_table), q.dtype
     if block_table.shape[0] != batch.B:
         raise ValueError(f"block_table has {block_table.shape[0]} rows, not {batch.B}")
     _call("lora_kv_attend", stream, (q, out, batch.buf, block_table, cache.data, ws),
           _heads(q, "q", batch.T, cache.head_dim, dtype), _heads(out, "out", batch.T, cache.head_dim, dtype), batch.T, batch.B,
-          _code(dtype), batch.ref, table, max(block_table.stride(0), width), width, cache.ref, scale, ws.data_ptr(),
+          _code(dtype), batch.ref, table, stride, width, cache.ref, scale, ws.data_ptr(),
           ws.numel() * ws.element_size())
 
 

@@ -415,3 +415,27 @@ def test_reference_cache_round_trip():
         for x, g in ((k, gk), (v, gv)):
             c, b = R.quantise(x.reshape(20, 2, -1, 32))
             assert np.array_equal(g.reshape(20, 2, -1, 32), R.values(c, b))
+
+
+def test_binding_refuses_block_tables_whose_rows_overlap():
+    """A row stride below the width (an expanded row, overlapping rows) would address rows behind the tensor."""
+    pos, b = torch.zeros(4, dtype=torch.int32), kv.Batch(8, 4, 4, 2, 64, device="cpu")
+    data = torch.zeros((4, kv.block_bytes(16, 2, 64)), dtype=torch.uint8)
+    cache, ws = kv.Cache(data, 16, 2, 64), kv.attend_workspace(b)
+    b._resize(4, 4)
+    q = torch.zeros((4, 4, 64), dtype=torch.bfloat16)
+    row = torch.zeros((1, 8), dtype=torch.int32)
+    for bad in (row.expand(4, 8), torch.as_strided(torch.zeros(32, dtype=torch.int32), (4, 8), (7, 1))):
+        with pytest.raises(ValueError, match="block_table"):
+            kv.lora_kv_build(pos, pos, 4, bad, pos, 4, 16, b)
+        with pytest.raises(ValueError, match="block_table"):
+            kv.lora_kv_attend(q, torch.empty_like(q), b, bad, cache, 0.1, ws)
+    # rows apart, and a single row of any stride, go on to the check of the device
+    for good in (torch.zeros((4, 8), dtype=torch.int32), torch.zeros((4, 11), dtype=torch.int32)[:, :8]):
+        with pytest.raises(ValueError, match="GPU"):
+            kv.lora_kv_build(pos, pos, 4, good, pos, 4, 16, b)
+        with pytest.raises(ValueError, match="GPU"):
+            kv.lora_kv_attend(q, torch.empty_like(q), b, good, cache, 0.1, ws)
+    one = torch.as_strided(torch.zeros(8, dtype=torch.int32), (1, 8), (0, 1))
+    with pytest.raises(ValueError, match="GPU"):
+        kv.lora_kv_build(pos[:1], pos[:1], 4, one, pos, 4, 16, b)
