@@ -333,6 +333,8 @@ def lora_kv_attend(q: torch.Tensor, out: torch.Tensor, batch: Batch, block_table
     (table, stride, width), dtype = _table(block_table), q.dtype
     if block_table.shape[0] != batch.B:
         raise ValueError(f"block_table has {block_table.shape[0]} rows, not {batch.B}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     _call("lora_kv_attend", stream, (q, out, batch.buf, block_table, cache.data, ws),
           _heads(q, "q", batch.T, cache.head_dim, dtype), _heads(out, "out", batch.T, cache.head_dim, dtype), batch.T, batch.B,
           _code(dtype), batch.ref, table, stride, width, cache.ref, scale, ws.data_ptr(),

@@ -439,3 +439,17 @@ def test_binding_refuses_block_tables_whose_rows_overlap():
     one = torch.as_strided(torch.zeros(8, dtype=torch.int32), (1, 8), (0, 1))
     with pytest.raises(ValueError, match="GPU"):
         kv.lora_kv_build(pos[:1], pos[:1], 4, one, pos, 4, 16, b)
+
+
+def test_binding_refuses_workspaces_that_are_not_contiguous():
+    """An expanded tensor counts more elements than it has memory for."""
+    b = kv.Batch(8, 4, 4, 2, 64, device="cpu")
+    data = torch.zeros((4, kv.block_bytes(16, 2, 64)), dtype=torch.uint8)
+    cache, ws, table = kv.Cache(data, 16, 2, 64), kv.attend_workspace(b), torch.zeros((4, 8), dtype=torch.int32)
+    b._resize(4, 4)
+    q = torch.zeros((4, 4, 64), dtype=torch.bfloat16)
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(ws.numel()), torch.zeros(2 * ws.numel(), dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            kv.lora_kv_attend(q, torch.empty_like(q), b, table, cache, 0.1, bad)
+    with pytest.raises(ValueError, match="GPU"):
+        kv.lora_kv_attend(q, torch.empty_like(q), b, table, cache, 0.1, ws)
