@@ -165,8 +165,13 @@ lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int3
   if (B > batch->max_seqs || T > batch->max_tokens) return LORA_ERR_WORKSPACE;
   const BatchSizes z = batch_sizes(batch->max_tokens, batch->max_seqs, batch->num_q_heads, batch->num_kv_heads);
   // the call writes the batch while it reads its inputs
-  for (const int32_t* p : {ctx_len, new_len, (const int32_t*)block_table, free_blocks})
-    if (p >= batch->q_indptr && p < batch->q_indptr + z.total / 4) return LORA_ERR_INVALID_ARG;
+  auto meets_batch = [&](const int32_t* p, int64_t n) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p), own = reinterpret_cast<uintptr_t>(batch->q_indptr);
+    return n > 0 && from < own + z.total && from + 4 * (uint64_t)n > own;
+  };
+  if (meets_batch(ctx_len, B) || meets_batch(new_len, B) || meets_batch(free_blocks, num_free) ||
+      meets_batch(block_table, B > 0 ? (B - 1) * table_stride + table_width : 0))
+    return LORA_ERR_INVALID_ARG;
   BuildArgs A;
   A.ctx = ctx_len;
   A.add = new_len;

@@ -151,8 +151,8 @@ lora_status_t lora_kv_batch_init(void* buf, size_t bytes, int32_t max_tokens, in
  * T: rows of the step's tensors.  Rows behind the last request's (T larger
  * than the sum of new_len: a padded batch) get -1 everywhere and no call
  * touches them.
- * free_blocks may be NULL when num_free is 0.  No input may lie in the batch's
- * own buffer (the next step's ctx_len is a copy of kv_len, not kv_len).
+ * free_blocks may be NULL when num_free is 0.  No input may reach into the
+ * batch's own buffer (the next step's ctx_len is a copy of kv_len, not kv_len).
  * Errors: INVALID_ARG, WORKSPACE (B or T past the capacity), UNSUPPORTED
  * (block_tokens; num_blocks*block_tokens past 2^31), HIP. */
 lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t T,

@@ -453,3 +453,15 @@ def test_binding_refuses_workspaces_that_are_not_contiguous():
             kv.lora_kv_attend(q, torch.empty_like(q), b, table, cache, 0.1, bad)
     with pytest.raises(ValueError, match="GPU"):
         kv.lora_kv_attend(q, torch.empty_like(q), b, table, cache, 0.1, ws)
+
+
+@pytest.mark.parametrize("which,count", [("ctx", 4), ("new", 4), ("table", 3 * 8 + 8), ("free", 4)])
+def test_build_refuses_inputs_that_reach_into_its_batch(which, count):
+    """Not only those that start there.  `count`: entries that the call may touch."""
+    a = Args()
+    outside = a.p + (1 << 15)
+    assert kv.lib()["lora_kv_batch_init"](outside, 1 << 30, 64, 8, 8, 2, 64, ctypes.addressof(a.batch)) == 0
+    n = kv.lib()["lora_kv_batch_size"](64, 8, 8, 2, 64)
+    for at in (outside - 4, outside - 4 * (count - 1), outside + n - 4):
+        assert kv.lib()["lora_kv_build"](*build_args(a, **{which: at})) == -1
+    # one that ends where the batch begins passes this check and is refused for T alone
