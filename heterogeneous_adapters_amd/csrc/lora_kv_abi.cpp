@@ -162,6 +162,8 @@ lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int3
   if (num_free > 0 && !free_blocks) return LORA_ERR_INVALID_ARG;
   if (lora_status_t st = check_batch(batch)) return st;
   if (!block_tokens_ok(block_tokens) || (int64_t)num_blocks * block_tokens > 0x7fffffffll) return LORA_ERR_UNSUPPORTED;
+  // a request's tokens, and the attention's steps past its last, stay within 32 bits
+  if ((int64_t)table_width * block_tokens > (1 << 30)) return LORA_ERR_UNSUPPORTED;
   if (B > batch->max_seqs || T > batch->max_tokens) return LORA_ERR_WORKSPACE;
   const BatchSizes z = batch_sizes(batch->max_tokens, batch->max_seqs, batch->num_q_heads, batch->num_kv_heads);
   // the call writes the batch while it reads its inputs

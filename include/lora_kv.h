@@ -154,7 +154,8 @@ lora_status_t lora_kv_batch_init(void* buf, size_t bytes, int32_t max_tokens, in
  * free_blocks may be NULL when num_free is 0.  No input may reach into the
  * batch's own buffer (the next step's ctx_len is a copy of kv_len, not kv_len).
  * Errors: INVALID_ARG, WORKSPACE (B or T past the capacity), UNSUPPORTED
- * (block_tokens; num_blocks*block_tokens past 2^31), HIP. */
+ * (block_tokens; num_blocks*block_tokens past 2^31; table_width*block_tokens
+ * past 2^30), HIP. */
 lora_status_t lora_kv_build(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t T,
                             int32_t* block_table, int64_t table_stride, int32_t table_width,
                             const int32_t* free_blocks, int32_t num_free, int32_t num_blocks, int32_t block_tokens,

@@ -465,3 +465,11 @@ def test_build_refuses_inputs_that_reach_into_its_batch(which, count):
     for at in (outside - 4, outside - 4 * (count - 1), outside + n - 4):
         assert kv.lib()["lora_kv_build"](*build_args(a, **{which: at})) == -1
     # one that ends where the batch begins passes this check and is refused for T alone
+
+
+@pytest.mark.parametrize("bt", [16, 64, 256])
+def test_build_refuses_rows_of_more_than_2_30_tokens(bt):
+    """The kernels count a request's tokens, and steps past its last, in 32 bits."""
+    width = (1 << 30) // bt
+    for w, code in ((width, -4), (width + 1, -6), (1 << 30, -6)):  # the first is refused for its B alone
+        assert kv.lib()["lora_kv_build"](*build_args(Args(), B=9, width=w, stride=1 << 30, nb=16, bt=bt)) == code
