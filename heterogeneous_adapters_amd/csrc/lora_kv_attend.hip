@@ -113,7 +113,7 @@ struct Item {
   int begin, end, chunks;     // keys of this item, items of the tile
 };
 // The descriptor is read along with the counters it is checked against (the
-// grid stays within the list's capacity), so that one trip to memory serves
+// grid, class_cap, is at most item_cap), so that one trip to memory serves
 // both.  `rows`: rows that the kernel takes of the tile, from row0 + skip on.
 __device__ __forceinline__ bool read_item(const AttendArgs& A, int cls, int count_at, int item, int skip, int rows, Item& it) {
   const int4* d = A.items + 2 * ((int64_t)cls * A.item_cap + item);

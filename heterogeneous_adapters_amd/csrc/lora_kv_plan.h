@@ -62,11 +62,16 @@ inline int64_t item_cap(int64_t T, int64_t B, int64_t hkv, int64_t G) {
   return kTargetItems / hkv + 1 + T * G / kUnit + 1 + B;
 }
 // The same for one class of a step with T tokens and B requests: its launch's
-// grid (a work-group without an item costs a launch slot: 9.5 us for 5768).
+// grid (a work-group without an item costs a launch slot: 9.5 us for 5768), at
+// most item_cap of any batch that holds the step.  Requests of class 1 have two
+// tiles at most, and more than 16 rows for each but the one that T cuts short.
 inline int64_t class_cap(int c, int64_t T, int64_t B, int64_t hkv, int64_t G) {
   const int64_t split = kTargetItems / hkv + 1;
   if (c == 0) return T > B ? split + B : item_cap(T, B, hkv, G);
-  if (c == 1) return split + (kMidMost / kMidRows) * B;
+  if (c == 1) {
+    const int64_t by_seqs = (kMidMost / kMidRows) * B, by_rows = T * G / kUnit + 1;
+    return split + (by_seqs < by_rows ? by_seqs : by_rows);
+  }
   return split + T * G / kWideRows + B;
 }
 // Room for partial results (16 rows of one chunk each).  A decode step needs

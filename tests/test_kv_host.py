@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -473,3 +474,73 @@ def test_build_refuses_rows_of_more_than_2_30_tokens(bt):
     width = (1 << 30) // bt
     for w, code in ((width, -4), (width + 1, -6), (1 << 30, -6)):  # the first is refused for its B alone
         assert kv.lib()["lora_kv_build"](*build_args(Args(), B=9, width=w, stride=1 << 30, nb=16, bt=bt)) == code
+
+
+# ----------------------------------------------------- the plan's arithmetic
+PLAN = r"""
+#include "lora_kv_plan.h"
+using namespace lora::kv;
+extern "C" {
+long long plan_item_cap(long long T, long long B, long long hkv, long long G) { return item_cap(T, B, hkv, G); }
+long long plan_class_cap(int c, long long T, long long B, long long hkv, long long G) { return class_cap(c, T, B, hkv, G); }
+int plan_even_chunk(int kv, int chunk) { return even_chunk(kv, chunk); }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    at = tmp_path_factory.mktemp("plan")
+    (at / "plan.cpp").write_text(PLAN)
+    csrc = os.path.join(ROOT, "heterogeneous_adapters_amd", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", f"-I{csrc}", str(at / "plan.cpp"), "-o", str(at / "plan.so")], check=True)
+    lib = ctypes.CDLL(str(at / "plan.so"))
+    lib.plan_item_cap.restype = lib.plan_class_cap.restype = ctypes.c_longlong
+    lib.plan_item_cap.argtypes, lib.plan_class_cap.argtypes = [ctypes.c_longlong] * 4, [ctypes.c_int] + [ctypes.c_longlong] * 4
+    return lib
+
+
+@pytest.mark.parametrize("hkv,G", [(1, 1), (8, 1), (8, 4), (2, 17), (32, 1), (1, 32), (128, 2), (1, 1024), (1024, 1)])
+def test_a_launch_stays_within_its_list_of_items(plan, hkv, G):
+    """Each class's grid is no longer than the list its descriptors are read from, whatever the step and the batch's capacity."""
+    for B in (1, 2, 3, 17, 100, 1000, 5000):
+        for T in (1, 2, B - 1, B, B + 1, B + 17, 2 * B, 16 * B, 1000 * B):
+            if T < 1:
+                continue
+            for most_t, most_b in ((T, B), (T + 5, B), (T, B + 9)):
+                room = plan.plan_item_cap(most_t, most_b, hkv, G)
+                for c in range(3) if T > B else (0,):  # the launches of the step
+                    assert plan.plan_class_cap(c, T, B, hkv, G) <= room, (c, T, B)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_a_launch_covers_its_items(plan, seed):
+    """The items of a step, by the plan's rules, are no more than the work-groups of each class's launch."""
+    rng = np.random.default_rng(seed)
+    for _ in range(30):
+        hkv, G = int(rng.choice([1, 2, 8, 32, 128])), int(rng.choice([1, 2, 4, 7, 16, 33]))
+        B = int(np.exp(rng.uniform(0, 6)))
+        new = np.floor(np.exp(rng.uniform(0, rng.choice([0.1, 2.0, 6.0]), B)) - rng.choice([0.0, 0.6])).astype(np.int64)
+        ctx = np.floor(np.exp(rng.uniform(0, 10, B)) - 1).astype(np.int64)
+        T = int(rng.integers(1, max(new.sum(), 1) + 2)) if rng.random() < 0.3 else int(new.sum()) + int(rng.integers(0, 3))
+        add = np.minimum(new, T)
+        many = T > B
+        last = np.minimum(np.cumsum(add), T)
+        rows = np.diff(np.concatenate([[0], last])) * G
+        cls = np.where((add * G <= 16) | (not many), 0, np.where(add * G <= 64, 1, 2))
+        per = np.array([16, 32, 128])[cls]
+        chunk = np.zeros(3, np.int64)
+        for group, target in (((0, 1), 1024), ((2,), 512)):
+            mine = np.isin(cls, group)
+            reads = int((-(-(add * G) // per) * (ctx + add))[mine].sum())
+            chunk[list(group)] = max(-(-(-(-reads * hkv // target)) // 256) * 256, 1024)
+        items = np.zeros(3, np.int64)
+        for i in range(B):
+            kv_i = int(ctx[i] + rows[i] // G)
+            even = plan.plan_even_chunk(kv_i, int(chunk[cls[i]]))
+            items[cls[i]] += -(-int(rows[i]) // per[i]) * max(-(-kv_i // even), 1)
+        for c in range(3):
+            if c == 0 or many:
+                assert items[c] <= plan.plan_class_cap(c, T, B, hkv, G), (c, T, B, hkv, G)
+            else:
+                assert items[c] == 0
