@@ -79,6 +79,12 @@ inline int64_t class_cap(int c, int64_t T, int64_t B, int64_t hkv, int64_t G) {
 // parts find no room are not split.
 inline int64_t part_cap(int64_t hkv) { return 8 * (kTargetItems / hkv + 1); }
 
+// Last of `rows` rows from `first` on, of `len`; -1 where there are none, so that
+// `key <= last_row` and `row <= last_row` hold for no key and no row.
+LORA_KV_HD inline int last_row(int first, int rows, int len) {
+  return first >= len ? -1 : (first + rows < len ? first + rows : len) - 1;
+}
+
 // An item is two int4: {request, first row, chunk, first part of the tile or
 // -1 (not split)} and {first token row, rows of the request, position of its
 // first token, cached tokens}.

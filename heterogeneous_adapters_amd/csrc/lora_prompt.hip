@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
   const int row_first = sp.tile * kRows + wave * kRowsPerWave;
   const int row = row_first + n;
-  const int row_last = min(row_first + kRowsPerWave, sp.len) - 1;  // below row_first: no rows in this wave
+  const int row_last = last_row(row_first, kRowsPerWave, sp.len);  // -1: this wave only copies
   const int n_tiles = (min((sp.tile + 1) * kRows, sp.len) + kKeys - 1) / kKeys;
 
   bf16x8 qf[kSteps];
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(64 * W, D == 128 ? 3 : 2) void prompt_kernel(const 
   };
   l += __shfl_xor(l, 32);
   if (row <= row_last) write(1.0f / l, true);
-  if (!__any(odd != odd || is_far(m))) return;
+  if (row_last < 0 || !__any(odd != odd || is_far(m))) return;
 
   // The long way, straight from global memory, 32 keys a step: the finite part
   // of V as usual, then, for each sign and for NaN, a product that counts the

@@ -484,6 +484,7 @@ extern "C" {
 long long plan_item_cap(long long T, long long B, long long hkv, long long G) { return item_cap(T, B, hkv, G); }
 long long plan_class_cap(int c, long long T, long long B, long long hkv, long long G) { return class_cap(c, T, B, hkv, G); }
 int plan_even_chunk(int kv, int chunk) { return even_chunk(kv, chunk); }
+int plan_last_row(int first, int rows, int len) { return last_row(first, rows, len); }
 }
 """
 
@@ -544,3 +545,15 @@ def test_a_launch_covers_its_items(plan, seed):
                 assert items[c] <= plan.plan_class_cap(c, T, B, hkv, G), (c, T, B, hkv, G)
             else:
                 assert items[c] == 0
+
+
+def test_waves_without_rows_take_no_keys(plan):
+    """The steps over a prompt's keys that its waves of 32 rows take: those of the rows that are there."""
+    for n in (1, 5, 31, 32, 33, 64, 65, 97, 127, 128, 129, 4097):
+        for tile in range(-(-n // 128)):
+            for wave in range(4):
+                first = 128 * tile + 32 * wave
+                rows = min(max(n - first, 0), 32)
+                last = plan.plan_last_row(first, 32, n)
+                assert len(range(0, last + 1, 32)) == (-(-(first + rows) // 32) if rows else 0), (n, first)
+                assert [r for r in range(first, first + 32) if r <= last] == list(range(first, first + rows))
