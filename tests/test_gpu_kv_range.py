@@ -1,5 +1,7 @@
 """The attention operators over the rest of their range: weights that sum to
-one, scores far from zero, fp32 queries rotated in 64 bits."""
+one, scores far from zero, fp32 queries rotated in 64 bits,
+every head dim of the 128-row kernel, rows in several tiles of a decode step,
+items without room for partial results."""
 import math
 
 import numpy as np
@@ -8,7 +10,7 @@ import torch
 
 import kv_reference as R
 from heterogeneous_adapters_amd import kv
-from test_gpu_kv import DEV, Step, host, i32, normal, to_dev
+from test_gpu_kv import DEV, Step, host, i32, make_table, normal, to_dev
 from test_gpu_prompt import run_prompt
 
 pytestmark = pytest.mark.gpu
@@ -189,3 +191,105 @@ def test_fp32_queries_are_rotated_in_64_bits_and_rounded_once(T, hq, hk, D, rot,
         # (a turn rounded to 53 bits), 2^-13 of half a step
         got = host(got)
         assert np.all(np.abs(got - want) <= 2 * 2.0 ** -24 * np.abs(want)) and np.mean(got != want) < 1e-3
+
+
+# ------------------------------------------------- head dims, tiles and splits
+class Big:
+    """A step over a cache of random bytes; the plain result in 64 bits on the GPU from the gathered values."""
+
+    def __init__(self, seed, ctx, new, hq, hkv, D, bt, dtype="bf16", pad=0):
+        rng = np.random.default_rng(seed)
+        self.ctx, self.new, self.hq, self.hkv, self.D = np.array(ctx), np.array(new), hq, hkv, D
+        table, free, num = make_table(rng, ctx, new, bt)
+        self.T = int(np.sum(new)) + pad
+        nc = D // 32
+        data = rng.integers(0, 256, (num, hkv * bt // 16, 544 * nc)).astype(np.uint8)
+        data[..., 512 * nc:] = 125 + data[..., 512 * nc:] % 3
+        self.cache = kv.Cache(torch.tensor(data.reshape(num, -1), device=DEV), bt, hkv, D)
+        self.batch = kv.Batch(self.T, len(ctx), hq, hkv, D)
+        self.table = i32(table)
+        self.q = to_dev(rng.standard_normal((self.T, hq, D)), dtype)
+        self.ws = kv.attend_workspace(self.batch)
+        kv.lora_kv_build(i32(ctx), i32(new), self.T, self.table, i32(free), num, bt, self.batch)
+        self.bt, self.dtype = bt, dtype
+
+    def check(self, q, out, scale):
+        kv.lora_kv_attend(q, out, self.batch, self.table, self.cache, scale, self.ws)
+        torch.cuda.synchronize()
+        assert int(self.batch.flags) == 0
+        begin, G = 0, self.hq // self.hkv
+        for i, (c, n) in enumerate(zip(self.ctx.tolist(), self.new.tolist())):
+            L = c + n
+            p = torch.arange(L, device=DEV)
+            slots = (self.table[i].long()[p // self.bt] * self.bt + p % self.bt).int()
+            k = torch.zeros((L, self.hkv, self.D), dtype=torch.float32, device=DEV)
+            v = torch.zeros_like(k)
+            kv.lora_kv_gather(self.cache, slots, k, v)
+            hide = p[None, :] > torch.arange(c, L, device=DEV)[:, None]
+            for h in range(self.hkv):
+                qq = self.q[begin:begin + n, h * G:(h + 1) * G].double().transpose(0, 1).contiguous()
+                kk, vv = k[:, h].double(), v[:, h].double()
+                x = (qq @ kk.T.contiguous() * scale).masked_fill(hide, -math.inf)
+                w = torch.softmax(x, -1)
+                o, a = w @ vv, w @ vv.abs()
+                s_abs = (qq.abs() @ kk.abs().T.contiguous() * scale).masked_fill(hide, 0.0).amax(-1, keepdim=True)
+                o, a, s_abs = (y.cpu().numpy() for y in (o, a, s_abs))
+                got = host(out[begin:begin + n, h * G:(h + 1) * G].transpose(0, 1))
+                bound = R.attend_bound(o, a, s_abs, L, self.D, self.dtype)
+                if self.dtype == "bf16":  # the sum is of rounded weights too
+                    bound = bound + 2.0 ** -8 * np.abs(o)
+                assert np.all(np.abs(got - o) <= bound), (i, h)
+            begin += n
+        return begin
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("D,hq,hkv,bt", [(128, 8, 2, 16), (128, 2, 2, 256), (160, 4, 2, 32), (192, 3, 1, 16), (224, 2, 1, 64), (256, 4, 2, 128)])
+def test_requests_of_many_rows_at_every_wide_head_dim(D, hq, hkv, bt, split, dtype):
+    ctx, new = ([2300, 0, 77], [131, 66, 1]) if split else ([150, 0, 77], [131, 66, 1])
+    s = Big(D + split, ctx, new, hq, hkv, D, bt, dtype, pad=3)
+    assert int(s.batch.counts[kv.COUNT_WIDE]) > 0 and (int(s.batch.counts[kv.COUNT_PARTS]) > 0) == split
+    out = torch.full_like(s.q, 5.0)
+    end = s.check(s.q, out, D ** -0.5)
+    assert bool((out[end:] == 5.0).all())
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (128, 8, 1), (256, 2, 1)])
+def test_requests_of_many_rows_with_strided_queries_and_outputs(D, hq, hkv):
+    s = Big(D, [1300, 20], [100, 70], hq, hkv, D, 16)
+    assert int(s.batch.counts[kv.COUNT_WIDE]) > 0
+    fused = torch.full((s.T, hq + 3, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    fused[:, 1:1 + hq] = s.q
+    out = torch.full((s.T, hq + 2, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    s.check(fused[:, 1:1 + hq], out[:, :hq], D ** -0.5)
+    assert bool((out[:, hq:] == 5.0).all())
+    first = torch.zeros((hq, s.T, D), dtype=torch.bfloat16, device=DEV).transpose(0, 1)  # heads first
+    s.check(s.q, first, D ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ctx,hq,hkv,D", [([5000, 3, 0], 32, 1, 64), ([4100, 900], 40, 1, 128), ([3000], 34, 2, 96), ([2100, 17], 17, 1, 256)])
+def test_decode_steps_with_more_query_heads_than_a_tile(ctx, hq, hkv, D, dtype):
+    s = Big(hq + D, ctx, [1] * len(ctx), hq, hkv, D, 16, dtype)
+    c = s.batch.counts
+    assert int(c[kv.COUNT_PARTS]) > 1 and int(c[kv.COUNT_MID]) + int(c[kv.COUNT_WIDE]) == 0
+    s.check(s.q, torch.zeros_like(s.q), D ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_long_chunk_among_idle_requests(dtype):
+    """As many requests as tokens: the step is planned as a decode step, in items of 16 rows."""
+    new = [0] * 100 + [60, 1]
+    s = Big(3, [20] * 100 + [1500, 40], new, 4, 2, 64, 16, dtype)
+    assert s.T <= len(new) and int(s.batch.counts[kv.COUNT_WIDE]) == 0
+    s.check(s.q, torch.zeros_like(s.q), 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_requests_without_room_for_partial_results_are_not_split(dtype):
+    hkv = 32
+    s = Big(4, [947, 1035] * 14 + [1035], [128, 40] * 14 + [40], hkv, hkv, 64, 16, dtype)
+    room = 8 * (1024 // hkv + 1)
+    assert int(s.batch.counts[kv.COUNT_PARTS]) > room
+    s.check(s.q, torch.zeros_like(s.q), 0.125)
