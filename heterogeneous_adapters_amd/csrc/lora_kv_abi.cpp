@@ -14,7 +14,8 @@ using namespace lora::kv;
 namespace {
 
 constexpr size_t kAlign = 256;
-// A launch has under 2^32 threads: work-groups of 512, four for a work item.
+// A launch has under 2^32 threads: work-groups of 256, up to four for a work
+// item, and a factor of two to spare.
 constexpr int64_t kMaxBlocks = (int64_t)1 << 23, kMaxItems = kMaxBlocks / 4;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -237,13 +238,12 @@ lora_status_t lora_rope_frequencies(int32_t rot_dim, double theta, int32_t scali
 
 // Work-groups of the rotation role for `heads` heads: enough head groups that
 // a small batch still spreads over the chip, whole passes of 256 threads else.
-static void rotation_geometry(RopeArgs& A, int heads, int dtype) {
+static void rotation_geometry(RopeArgs& A, int heads) {
   const int tiles = ceil_div_i(A.T, 4);
   int groups = std::max(1, std::min(heads, ceil_div_i(512, std::max(tiles, 1))));
   A.q_heads_per_group = ceil_div_i(heads, groups);
   A.q_groups = ceil_div_i(heads, A.q_heads_per_group);
   A.rot_blocks = tiles * A.q_groups;
-  (void)dtype;
 }
 
 // Work-groups of the cache role: 16 rows each, and as many groups of whole
@@ -284,7 +284,7 @@ lora_status_t lora_rope(const lora_heads_t* q, const lora_heads_t* q_out, const 
   A.D = head_dim;
   A.rot = rope->rot_dim;
   A.interleaved = rope->layout == LORA_ROPE_INTERLEAVED;
-  rotation_geometry(A, A.qo.heads + A.ko.heads, dtype);
+  rotation_geometry(A, A.qo.heads + A.ko.heads);
   return hip(launch_rope(A, dtype, A.rot_blocks, static_cast<hipStream_t>(stream)));
 }
 
@@ -324,7 +324,7 @@ lora_status_t lora_kv_append(const lora_heads_t* q, const lora_heads_t* q_out, c
   A.D = cache->head_dim;
   A.cache = cache_of(cache);
   A.flags = flags;
-  if (A.qo.heads > 0) rotation_geometry(A, A.qo.heads, dtype);
+  if (A.qo.heads > 0) rotation_geometry(A, A.qo.heads);
   const int cache_blocks = cache_geometry(A);
   return hip(launch_rope(A, dtype, A.rot_blocks + cache_blocks, static_cast<hipStream_t>(stream)));
 }

@@ -237,6 +237,9 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t* cache, const int32_t* slots,
  * that sees no token gets zeros; rows that belong to no request are not
  * written.  Tokens in blocks outside the cache, or past the table's width, are
  * not attended (LORA_KV_FLAG_BLOCK_RANGE in the batch's flags).
+ * A step with T <= B is planned as a decode step, in items of 16 rows, whatever
+ * its requests bring; where several bring long chunks among idle ones, leave
+ * the idle ones out or pad T past B.
  * B and T must be those of the batch's lora_kv_build, block_table as that call
  * left it, the cache of the same block_tokens.
  * ws: device, lora_kv_workspace_size(batch) bytes, 16-byte aligned.  The call
