@@ -14,9 +14,10 @@
 // v_mfma_f32_16x16x32_bf16: S^T = K Q^T, whose result layout (row = lane%16,
 // tokens 4g..4g+3 of each 16) is the B operand that O^T = V^T P^T needs, with
 // the record's V order supplying A, so P never leaves its registers.  It is
-// rounded to bf16 there, by up to 2^-8 of each weight (a second term would
-// double the second product); l sums the rounded weights, so that they sum to
-// one (no change in time).  fp32 rows and weights are split into three bf16
+// rounded to bf16 there, by up to 2^-8 of each weight (with a second term the
+// large decode step below takes 231 us against 222, and its error against 64
+// bits, of which rounding the result makes 0.0017, 0.0017 against 0.0020); l
+// sums the rounded weights, so that they sum to one (no change in time).  fp32 rows and weights are split into three bf16
 // terms (24 bits), the codes being exact.
 //
 // Measured on MI355X: 128 requests of up to 4097 tokens, 32 kv heads of 128,
@@ -491,10 +492,11 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename 
 // 16 tokens by each wave, into LDS, while the tile before is multiplied with
 // v_mfma_f32_32x32x16_bf16, 32 rows per wave.  K lies by token, V by dim in the
 // token order of P's registers, both XOR-swizzled in 16-byte pieces against
-// the 64 banks.  Four chunks of 512 tokens over 5000, 32 query heads: 213 to
-// 224 us, 680-710 TFLOP/s (16 rows at a time: 500 us; 32 rows without LDS:
-// 292), bound by the issue of conversions and exponentials (48 % of the time)
-// and products (41 %).
+// the 64 banks.  Four chunks of 512 tokens over 5000, 32 query heads: 214 to
+// 225 us, 670-710 TFLOP/s (32 rows without LDS: 292).  Two waves share a SIMD;
+// while a compute unit is busy, conversions and exponentials take 45 % of its
+// SIMDs' time and products 41 %, and units are busy for about 70 % of the launch:
+// the chunks' work-groups are all resident at once and end at different times.
 template <int NC>
 __global__ __launch_bounds__(256, 2) void attend_wide_kernel(const AttendArgs A) {
   constexpr int D = 32 * NC, kThreads = 256, kKeys = 64, kUnits = kWideRows / kUnit;

@@ -10,7 +10,9 @@ namespace kv {
 constexpr int kUnit = 16;        // tokens per cache record, rows per attention tile
 constexpr int kTile = 32;        // cached tokens per step of a wave
 constexpr int kChunkStep = 256;  // chunks are multiples of this: two steps of each of 4 waves
-constexpr int kMinChunk = 1024;   // smallest chunk of cached tokens per work item
+// Smallest chunk of cached tokens per work item (one request of 32768 tokens:
+// 22.5 us with 1024, 25.6 with 512, 24.6 with 2048; other steps within 2 %).
+constexpr int kMinChunk = 1024;
 // Work items (over all kv heads) that the plan aims for.
 constexpr int kTargetItems = 1024;
 // The same for items of 128 rows, two of which fill a compute unit and whose
@@ -25,8 +27,8 @@ constexpr int kCountTokens = 0, kCountNewBlocks = 1, kCountItems = 2, kCountPart
 // kv head): up to 16 rows, one matrix tile; up to 64, two tiles on the same
 // converted keys; more, 128 rows that share the conversion through LDS.  The
 // last two only where a step brings more tokens than requests (what the host
-// knows of it, so that a decode step launches one kernel: the other two, without
-// items, would add 7 us to its 12 or 16).  Chunks of 512 over 4488 tokens, 32
+// knows of it, so that a decode step, of 12 us or more, launches one kernel; a
+// launch without items takes 4.5 us of the mixed step).  Chunks of 512 over 4488 tokens, 32
 // heads on 8 of 128, among as many idle requests as tokens: four of them 311 us
 // in 16-row items, 201 with T padded past B; one 89 and 99.
 constexpr int kClasses = 3;

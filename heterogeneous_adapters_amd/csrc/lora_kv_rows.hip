@@ -18,8 +18,8 @@
 // One launch: work-groups of the rotation role walk (token, head, vector) of
 // Q (and of K in lora_rope), those of the cache role (16 tokens, a share of
 // the heads).  Both read and write each byte once; the bound is HBM: 38781
-// tokens of 32 + 8 heads of 128 take 217 us (3.9 TB/s of the 4.7 that a copy
-// reaches), their gather 40 us.  A few tokens are bound by the chain position
+// tokens of 32 + 8 heads of 128 take 225 us (3.7 TB/s of the 4.7 that a copy
+// reaches), their gather 43 us; 8192 fp32 tokens 82.  A few tokens are bound by the chain position
 // -> angle -> product: 9 us for 16, of which a launch alone is 3.
 #include "lora_kv_dev.h"
 #include "lora_kv_host.h"

@@ -3,7 +3,9 @@
 // Mathematics: per row one pass over the keys with a running maximum m and
 // sum l of exp2(s - m), s = scale log2(e) q.k.  2 * sum L^2 * heads * D
 // flops: bound by the issue of products and of the softmax's vector
-// instructions, which share a SIMD's time (56 % and 45 % of it).
+// instructions (long prompts: 62 % and 49 % of a SIMD's time, beside each other
+// for a tenth of it at least); many shorter ones by starts, diagonals and
+// barriers too (42 % and 40 %).
 //
 // bf16: a work-group of 4 waves takes 32 rows per wave of one query head and
 // walks the prompt's keys in tiles of 32 or 64, copied straight into LDS
@@ -23,9 +25,9 @@
 // what those of unrounded weights did (8192 tokens 616 us against 621).
 //
 // Measured on MI355X: prompts of 8192, 4097 and 1 tokens, 32 query heads of
-// 128 on 8 kv heads, 610 us = 1.12 PFLOP/s of causal work (the installed
-// library's plain product reaches 1.21); 32 prompts of 128..2048 with 32 kv
-// heads 520 us.  Four waves per work-group: three of them share a CU out of
+// 128 on 8 kv heads, 620 us = 1.11 PFLOP/s of causal work (the installed
+// library's plain product reaches 1.2); 32 prompts of 128..2048 with 32 kv
+// heads 505 us.  Four waves per work-group: three of them share a CU out of
 // step (8 waves: 683 against 658).
 //
 // fp32 (validation): one wave per 16 rows on v_mfma_f32_16x16x4_f32, keys and
@@ -45,9 +47,9 @@ constexpr int kRowsPerWave = 32;
 
 // Keys per tile.  32 halve the scores in flight, which buys a third wave per
 // SIMD at 128 dims and saves registers from spilling to the other bank above
-// (8192 keys at 128 dims: 630 us against 640; 4096 at 192: 126 against 148).
+// (8192 keys at 128 dims: 609 us against 624; 4096 at 192: 135 against 141).
 // Below 128 registers are no bound and 64 keys per barrier win (64 dims, 8192
-// keys: 305 against 331); at 256 either spills and 64 lose less.
+// keys: 306 against 326); at 256 so do they (4096 keys: 183 against 458).
 constexpr int keys_per_tile(int D) { return D >= 128 && D < 256 ? 32 : 64; }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
