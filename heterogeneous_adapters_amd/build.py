@@ -19,7 +19,9 @@ SOURCES = [os.path.join(CSRC, "lora_kernels.hip"), os.path.join(CSRC, "lora_abi.
            os.path.join(CSRC, "lora_pool.cpp"), os.path.join(CSRC, "lora_noalloc.hip"),
            os.path.join(CSRC, "lora_kv_abi.cpp"), os.path.join(CSRC, "lora_kv_batch.hip"),
            os.path.join(CSRC, "lora_kv_rows.hip"), os.path.join(CSRC, "lora_kv_attend.hip"),
-           os.path.join(CSRC, "lora_prompt.hip")]
+           os.path.join(CSRC, "lora_prompt.hip"), os.path.join(CSRC, "lora_kv_share.hip"),
+           os.path.join(CSRC, "lora_beam_abi.cpp"), os.path.join(CSRC, "lora_beam_select.hip"),
+           os.path.join(CSRC, "lora_beam_moves.hip")]
 ARCH = "gfx950"
 
 

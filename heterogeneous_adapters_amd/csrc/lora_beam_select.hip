@@ -1,0 +1,270 @@
+// lora_beam_select: the best continuations of every request's beams.
+//
+// Mathematics: a row's candidates are ordered as its logits are, so a row needs
+// its `beams` highest logits and log(sum e^x), both from one pass: a wave
+// holds 2048 logits in registers, sums e^(x - r) against its highest logit r so
+// far (each chunk's sum in fp32 per lane, the chunks' in fp64) and keeps the
+// highest logits so far, one per lane in descending order, as keys (the logit
+// as an ordered integer, then the token's complement, so that equal logits go
+// by the lower token).  A chunk whose highest logit is below the last of these
+// is done with its sum.  A second launch joins the waves of each row and ranks the request's
+// beams * beams candidates in 64 bits.
+#include "lora_beam_args.h"
+#include "lora_kv_dev.h"
+
+namespace lora {
+namespace beam {
+
+using namespace lora::kv;
+
+namespace {
+
+constexpr float kLog2eHi = 1.44269502162933349609375f;  // log2(e) to 24 bits, and the rest
+constexpr float kLog2eLo = 1.92596299112661746887e-08f;
+
+// e^d for d <= 0, -inf among them: off by the rounding of d log2(e), 2^-24 of
+// it either way, and of exp2.
+__device__ __forceinline__ float exp_of(float d) { return exp2_hw(fmaf(d, kLog2eLo, d * kLog2eHi)); }
+
+// Floats as integers of the same order; 0 is below every one that stands for a logit.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t kMinusInf = 0x007fffffu;  // ordered(-inf)
+
+__device__ __forceinline__ uint64_t shfl64(uint64_t x, int lane) {
+  return (uint64_t)(uint32_t)__shfl((int)(uint32_t)x, lane) | (uint64_t)(uint32_t)__shfl((int)(x >> 32), lane) << 32;
+}
+__device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {  // a uniform lane
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32;
+}
+
+// The highest n keys seen so far, lane i the i-th; 0 where there are none.
+struct Best {
+  uint64_t list = 0, least = 0;  // least: the n-th, uniform
+  __device__ __forceinline__ void put(uint64_t key, int n) {  // a uniform key above `least`
+    const int lane = threadIdx.x & 63;
+    const int at = __popcll(__ballot(list > key));
+    const uint64_t up = shfl64(list, max(lane - 1, 0));
+    list = lane < at ? list : lane == at ? key : up;
+    least = lane64(list, n - 1);
+  }
+};
+
+// The n-th highest of the lanes' values.
+__device__ __forceinline__ uint32_t nth_highest(uint32_t x, int n) {
+  uint32_t t = 0;
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t up = t | 1u << b;
+    if (__popcll(__ballot(x >= up)) >= n) t = up;
+  }
+  return t;
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
+  typedef typename E::T T;
+  constexpr int kEpv = E::kEpv, kVecs = 32 / kEpv;
+  const int lane = threadIdx.x & 63;
+  const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int row = uniform((int)(job / A.waves)), wave = uniform((int)(job - (int64_t)row * A.waves));
+  if (row >= A.requests * A.beams) return;
+  const float score = A.score[row];
+  if (A.done[row] != 0 || !(fabsf(score) < INFINITY)) return;  // not continued
+
+  const T* x = static_cast<const T*>(A.logits) + row * A.stride;
+  // vectors start before the row where its first logit is not aligned
+  const int skew = (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % kEpv);
+  const int first = wave * A.chunks, last = min(first + A.chunks, (A.vocab + skew + kChunk - 1) / kChunk);
+
+  Best best;
+  float ref = -INFINITY;  // the highest logit so far
+  double sum = 0.0;       // of e^(x - ref), this lane's share
+  bool odd = false;
+  u32x4 raw[kVecs] = {};
+  auto vec_at = [&](int chunk, int v) { return chunk * kChunk + (v * 64 + lane) * kEpv - skew; };
+  auto load = [&](int chunk) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int at = vec_at(chunk, v);
+      if (at >= 0 && at + kEpv <= A.vocab) raw[v] = *reinterpret_cast<const u32x4*>(x + at);
+    }
+  };
+  if (first < last) load(first);
+  for (int chunk = first; chunk < last; ++chunk) {
+    float y[32];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      float part[kEpv];
+      unpack(raw[v], part);
+#pragma unroll
+      for (int i = 0; i < kEpv; ++i) y[v * kEpv + i] = part[i];
+    }
+    if (chunk + 1 < last) load(chunk + 1);
+    if (chunk * kChunk < skew || (chunk + 1) * kChunk - skew > A.vocab) {  // an end of the row: vectors that are not whole
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const int at = vec_at(chunk, v);
+        if (at >= 0 && at + kEpv <= A.vocab) continue;
+#pragma unroll
+        for (int i = 0; i < kEpv; ++i) y[v * kEpv + i] = at + i >= 0 && at + i < A.vocab ? to_f(x[at + i]) : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(y[i] < INFINITY)) odd = true, y[i] = -INFINITY;
+
+    float most = y[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) most = fmaxf(most, y[i]);
+    float top = most;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if (top == -INFINITY) continue;
+    if (top > ref) {
+      sum *= exp((double)ref - (double)top);  // 0 at first
+      ref = top;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += exp_of(y[i] - ref);
+    sum += (double)s;
+
+    // candidates
+    uint32_t bound = (uint32_t)(best.least >> 32);
+    const uint32_t high = ordered(most + 0.0f);
+    if (!__any(high >= bound)) continue;
+    if (bound == 0) bound = max(nth_highest(high, A.beams), kMinusInf + 1);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t k = ordered(y[i] + 0.0f);  // one zero
+      uint64_t mask = __ballot(k >= bound);
+      while (mask) {
+        const int from = __ffsll((long long)mask) - 1;
+        mask &= mask - 1;
+        const int token = chunk * kChunk + ((i / kEpv) * 64 + from) * kEpv + i % kEpv - skew;
+        const uint64_t key = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)k, from) << 32 | (uint32_t)~token;
+        if (key > best.least) {
+          best.put(key, A.beams);
+          bound = max(bound, (uint32_t)(best.least >> 32));
+        }
+      }
+    }
+  }
+  if (__any(odd) && lane == 0 && A.flags) atomicOr(A.flags, LORA_BEAM_FLAG_LOGITS);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  const int64_t at = (int64_t)row * A.waves + wave;
+  if (lane < A.beams) A.keys[at * A.beams + lane] = best.list;
+  if (lane == 0) A.sums[2 * at] = ref, A.sums[2 * at + 1] = sum;
+}
+
+// One work-group per request.
+__global__ __launch_bounds__(256) void pick_kernel(const SelectArgs A) {
+  constexpr int kMost = LORA_BEAM_MAX;
+  __shared__ double s_rank[kMost * kMost], s_total[kMost * kMost];
+  __shared__ int32_t s_token[kMost * kMost];
+  __shared__ float s_score[kMost];
+  __shared__ int32_t s_length[kMost], s_done[kMost], s_chosen;
+  const int W = A.beams, row0 = blockIdx.x * W;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x < W) {
+    s_score[threadIdx.x] = A.score[row0 + threadIdx.x];
+    s_length[threadIdx.x] = A.length[row0 + threadIdx.x];
+    s_done[threadIdx.x] = A.done[row0 + threadIdx.x];
+  }
+  if (threadIdx.x == 0) s_chosen = 0;
+  __syncthreads();
+  for (int w = wave; w < W; w += 4) {
+    const float score = s_score[w];
+    const bool live = fabsf(score) < INFINITY, done = s_done[w] != 0;
+    double total = -INFINITY;
+    int token = -1;
+    if (live && done) {
+      if (lane == 0) total = score, token = A.eos;
+    } else if (live) {
+      const int64_t at = (int64_t)(row0 + w) * A.waves;
+      double ref = -INFINITY;
+      for (int i = lane; i < A.waves; i += 64) ref = fmax(ref, A.sums[2 * (at + i)]);
+#pragma unroll
+      for (int d = 32; d; d >>= 1) ref = fmax(ref, __shfl_xor(ref, d));
+      double sum = 0.0;
+      for (int i = lane; i < A.waves; i += 64) {
+        const double r = A.sums[2 * (at + i)];
+        if (r > -INFINITY) sum += A.sums[2 * (at + i) + 1] * exp(r - ref);
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+      Best best;
+      const int keys = A.waves * W;
+      for (int i0 = 0; i0 < keys; i0 += 64) {
+        const uint64_t key = i0 + lane < keys ? A.keys[at * W + i0 + lane] : 0;
+        uint64_t mask = __ballot(key > best.least);
+        while (mask) {
+          const int from = __ffsll((long long)mask) - 1;
+          mask &= mask - 1;
+          const uint64_t k = lane64(key, from);
+          if (k > best.least) best.put(k, W);
+        }
+      }
+      if (lane < W && best.list) {
+        total = (double)score + ((double)from_ordered((uint32_t)(best.list >> 32)) - ref - log(sum));
+        token = (int)~(uint32_t)best.list;
+      }
+    }
+    if (lane < W) {
+      double rank = total;
+      if (A.penalty != 0.0) rank = total / pow((double)max(s_length[w] + (done ? 0 : 1), 1), A.penalty);
+      s_rank[w * W + lane] = rank, s_total[w * W + lane] = total, s_token[w * W + lane] = token;
+    }
+  }
+  __syncthreads();
+  // each candidate's place: those of a row lie in their order
+  const int all = W * W;
+  for (int i = threadIdx.x; i < all; i += 256) {
+    const double rank = s_rank[i];
+    if (!(s_total[i] > -INFINITY)) continue;
+    int before = 0;
+    for (int j = 0; j < all; ++j) {
+      const double other = s_rank[j];
+      before += s_total[j] > -INFINITY && (other > rank || (other == rank && j < i));
+    }
+    if (before >= W) continue;
+    atomicAdd(&s_chosen, 1);
+    const int w = i / W, to = row0 + before, token = s_token[i];
+    const bool done = s_done[w] != 0;
+    A.parent[to] = row0 + w;
+    A.token[to] = token;
+    A.score_out[to] = (float)s_total[i];
+    A.length_out[to] = s_length[w] + (done ? 0 : 1);
+    A.done_out[to] = done || (token == A.eos && A.eos >= 0);
+  }
+  __syncthreads();
+  if (threadIdx.x >= s_chosen && threadIdx.x < W) {
+    const int to = row0 + threadIdx.x;
+    A.parent[to] = -1;
+    A.token[to] = -1;
+    A.score_out[to] = -INFINITY;
+    A.length_out[to] = 0;
+    A.done_out[to] = 1;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_select(const SelectArgs& A, int dtype, hipStream_t s) {
+  const int64_t jobs = (int64_t)A.requests * A.beams * A.waves;
+  const unsigned blocks = (unsigned)((jobs + 3) / 4);
+  if (dtype == LORA_DTYPE_BF16) rows_kernel<Bf16><<<blocks, 256, 0, s>>>(A);
+  else rows_kernel<F32><<<blocks, 256, 0, s>>>(A);
+  pick_kernel<<<A.requests, 256, 0, s>>>(A);
+  return hipGetLastError();
+}
+
+}  // namespace beam
+}  // namespace lora

@@ -106,6 +106,31 @@ lora_status_t check_batch(const lora_kv_batch_t* b) {
                                                                                             : LORA_ERR_INVALID_ARG;
 }
 
+// A shared plan's buffer: counts; per group its prefix's tokens, first request
+// and results; per request its results; items.
+struct ShareSizes {
+  size_t counts, group, group_parts, seq_parts, items, total;
+};
+bool share_ok(const lora_kv_batch_t* b, int32_t max_groups) {
+  const int64_t hkv = b->num_kv_heads, G = b->num_q_heads / hkv;
+  return max_groups >= 0 && max_groups <= b->max_seqs && share_row_cap(b->max_tokens, hkv, G) < 0x7fffffffll &&
+         share_item_cap(b->max_tokens, b->max_seqs, max_groups, hkv, G) * hkv < kMaxItems;
+}
+ShareSizes share_sizes(const lora_kv_batch_t* b, int32_t max_groups) {
+  const int64_t hkv = b->num_kv_heads, G = b->num_q_heads / hkv;
+  ShareSizes z;
+  z.counts = align_up(4 * kNumShare);
+  z.group = align_up(4 * (size_t)max_groups);
+  z.group_parts = align_up(16 * (size_t)max_groups);
+  z.seq_parts = align_up(32 * (size_t)b->max_seqs);
+  z.items = kLists * kShareItem * 16 * (size_t)share_item_cap(b->max_tokens, b->max_seqs, max_groups, hkv, G);
+  z.total = align_up(z.counts + 2 * z.group + z.group_parts + z.seq_parts + z.items);
+  return z;
+}
+lora_status_t check_share(const lora_kv_batch_t* b, const lora_kv_share_t* s) {
+  return s && s->counts && s->plan && share_ok(b, s->max_groups) ? LORA_OK : LORA_ERR_INVALID_ARG;
+}
+
 lora_status_t hip(hipError_t e) { return e == hipSuccess ? LORA_OK : LORA_ERR_HIP; }
 
 }  // namespace
@@ -354,10 +379,10 @@ size_t lora_kv_workspace_size(const lora_kv_batch_t* b) {
   return align_up((size_t)part_cap(b->num_kv_heads) * b->num_kv_heads * kUnit * (b->head_dim + 2) * sizeof(float));
 }
 
-lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32_t T, int32_t B, int32_t dtype,
-                             const lora_kv_batch_t* batch, const int32_t* block_table, int64_t table_stride,
-                             int32_t table_width, const lora_kv_cache_t* cache, float scale, void* ws,
-                             size_t ws_bytes, void* stream) {
+// What lora_kv_attend and lora_kv_attend_shared check and pass on alike.
+static lora_status_t attend_args(const lora_heads_t* q, const lora_heads_t* o, int32_t T, int32_t B, int32_t dtype,
+                                 const lora_kv_batch_t* batch, const int32_t* block_table, int64_t table_stride,
+                                 int32_t table_width, const lora_kv_cache_t* cache, float scale, AttendArgs& A) {
   if (T < 0 || B < 0 || table_width < 0) return LORA_ERR_INVALID_ARG;
   if (B > 0 && (!block_table || table_width < 1 || table_stride < table_width)) return LORA_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || !isfinite(scale)) return LORA_ERR_INVALID_ARG;
@@ -370,12 +395,7 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
       cache->head_dim != batch->head_dim || (q->data == o->data && T > 0))
     return LORA_ERR_INVALID_ARG;
   if (T > batch->max_tokens || B > batch->max_seqs) return LORA_ERR_WORKSPACE;
-  if (!ws) return LORA_ERR_INVALID_ARG;
-  if (ws_bytes < lora_kv_workspace_size(batch)) return LORA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return LORA_ERR_ALIGNMENT;
-  if (T == 0 || B == 0) return LORA_OK;
   const BatchSizes z = batch_sizes(batch->max_tokens, batch->max_seqs, batch->num_q_heads, batch->num_kv_heads);
-  AttendArgs A;
   A.q = rows_of(q);
   A.o = rows_of(o);
   A.counts = batch->counts;
@@ -390,8 +410,123 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
   A.item_cap = (int32_t)item_cap(batch->max_tokens, batch->max_seqs, batch->num_kv_heads, A.G);
   A.cache = cache_of(cache);
   A.scale_log2e = scale * 1.4426950408889634f;
+  return LORA_OK;
+}
+
+lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32_t T, int32_t B, int32_t dtype,
+                             const lora_kv_batch_t* batch, const int32_t* block_table, int64_t table_stride,
+                             int32_t table_width, const lora_kv_cache_t* cache, float scale, void* ws,
+                             size_t ws_bytes, void* stream) {
+  AttendArgs A;
+  if (lora_status_t st = attend_args(q, o, T, B, dtype, batch, block_table, table_stride, table_width, cache, scale, A))
+    return st;
+  if (!ws) return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < lora_kv_workspace_size(batch)) return LORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LORA_ERR_ALIGNMENT;
+  if (T == 0 || B == 0) return LORA_OK;
   A.part = static_cast<float*>(ws);
   return hip(launch_attend(A, dtype, many_rows(T, B), static_cast<hipStream_t>(stream)));
+}
+
+size_t lora_kv_share_size(const lora_kv_batch_t* batch, int32_t max_groups) {
+  if (check_batch(batch) || !share_ok(batch, max_groups)) return 0;
+  return share_sizes(batch, max_groups).total;
+}
+
+lora_status_t lora_kv_share_init(void* buf, size_t bytes, const lora_kv_batch_t* batch, int32_t max_groups,
+                                 lora_kv_share_t* out) {
+  if (!buf || !out || max_groups < 0) return LORA_ERR_INVALID_ARG;
+  if (lora_status_t st = check_batch(batch)) return st;
+  if (!share_ok(batch, max_groups)) return LORA_ERR_UNSUPPORTED;
+  if (!aligned16(buf)) return LORA_ERR_ALIGNMENT;
+  const ShareSizes z = share_sizes(batch, max_groups);
+  if (bytes < z.total) return LORA_ERR_WORKSPACE;
+  out->max_groups = max_groups;
+  out->counts = static_cast<int32_t*>(buf);
+  out->plan = out->counts + z.counts / 4;
+  return LORA_OK;
+}
+
+lora_status_t lora_kv_share(const int32_t* group_indptr, const int32_t* shared_len, int32_t num_groups, int32_t T,
+                            int32_t B, const lora_kv_batch_t* batch, const lora_kv_share_t* share, void* stream) {
+  if (T < 0 || B < 0 || num_groups < 0 || (num_groups > 0 && (!group_indptr || !shared_len))) return LORA_ERR_INVALID_ARG;
+  if (lora_status_t st = check_batch(batch)) return st;
+  if (lora_status_t st = check_share(batch, share)) return st;
+  if (T > batch->max_tokens || B > batch->max_seqs || num_groups > share->max_groups) return LORA_ERR_WORKSPACE;
+  const ShareSizes z = share_sizes(batch, share->max_groups);
+  // the call writes the plan, and the batch's flags, while it reads its inputs
+  const BatchSizes zb = batch_sizes(batch->max_tokens, batch->max_seqs, batch->num_q_heads, batch->num_kv_heads);
+  auto meets = [](const int32_t* p, int64_t n, const int32_t* to, size_t bytes) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p), own = reinterpret_cast<uintptr_t>(to);
+    return n > 0 && from < own + bytes && from + 4 * (uint64_t)n > own;
+  };
+  for (int k = 0; k < 2 && num_groups > 0; ++k) {
+    const int32_t* p = k ? shared_len : group_indptr;
+    if (meets(p, num_groups + 1 - k, share->counts, z.total) || meets(p, num_groups + 1 - k, batch->q_indptr, zb.total))
+      return LORA_ERR_INVALID_ARG;
+  }
+  ShareArgs A;
+  A.group_indptr = group_indptr;
+  A.shared_len = shared_len;
+  A.groups = num_groups;
+  A.B = B;
+  A.T = T;
+  A.hkv = batch->num_kv_heads;
+  A.G = batch->num_q_heads / batch->num_kv_heads;
+  A.prefix_class = prefix_class(T, A.G, num_groups);
+  A.item_cap = (int32_t)share_item_cap(batch->max_tokens, batch->max_seqs, share->max_groups, A.hkv, A.G);
+  A.row_cap = (int32_t)share_row_cap(batch->max_tokens, A.hkv, A.G);
+  A.q_indptr = batch->q_indptr;
+  A.kv_len = batch->kv_len;
+  A.positions = batch->positions;
+  A.counts = batch->counts;
+  A.share = share->counts;
+  A.cut = share->plan;
+  A.first = A.cut + z.group / 4;
+  A.group_parts = reinterpret_cast<int4*>(A.first + z.group / 4);
+  A.seq_parts = A.group_parts + z.group_parts / 16;
+  A.items = A.seq_parts + z.seq_parts / 16;
+  return hip(launch_share(A, static_cast<hipStream_t>(stream)));
+}
+
+// Partial results: rows of head_dim sums, then their maxima and sums of weights.
+static size_t share_row_bytes(const lora_kv_batch_t* b) {
+  return align_up((size_t)share_row_cap(b->max_tokens, b->num_kv_heads, b->num_q_heads / b->num_kv_heads) * b->num_kv_heads *
+                  b->head_dim * sizeof(float));
+}
+size_t lora_kv_share_workspace_size(const lora_kv_batch_t* b, const lora_kv_share_t* share) {
+  if (check_batch(b) || check_share(b, share)) return 0;
+  return share_row_bytes(b) + align_up(share_row_bytes(b) / b->head_dim * 2);
+}
+
+lora_status_t lora_kv_attend_shared(const lora_heads_t* q, const lora_heads_t* o, int32_t T, int32_t B,
+                                    int32_t num_groups, int32_t dtype, const lora_kv_batch_t* batch,
+                                    const lora_kv_share_t* share, const int32_t* block_table, int64_t table_stride,
+                                    int32_t table_width, const lora_kv_cache_t* cache, float scale, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  SharedArgs A;
+  if (num_groups < 0) return LORA_ERR_INVALID_ARG;
+  if (lora_status_t st = attend_args(q, o, T, B, dtype, batch, block_table, table_stride, table_width, cache, scale, A))
+    return st;
+  if (lora_status_t st = check_share(batch, share)) return st;
+  if (num_groups > share->max_groups) return LORA_ERR_WORKSPACE;
+  if (!ws) return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < lora_kv_share_workspace_size(batch, share)) return LORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LORA_ERR_ALIGNMENT;
+  if (T == 0 || B == 0) return LORA_OK;
+  const ShareSizes z = share_sizes(batch, share->max_groups);
+  const int4* parts = reinterpret_cast<const int4*>(share->plan + 2 * (z.group / 4));
+  A.item_cap = (int32_t)share_item_cap(batch->max_tokens, batch->max_seqs, share->max_groups, cache->num_kv_heads, A.G);
+  A.row_cap = (int32_t)share_row_cap(batch->max_tokens, cache->num_kv_heads, A.G);
+  A.share = share->counts;
+  A.seq_parts = parts + z.group_parts / 16;
+  A.items = A.seq_parts + z.seq_parts / 16;
+  A.token_seq = batch->token_seq;
+  A.groups = num_groups;
+  A.part = static_cast<float*>(ws);
+  A.part_ml = A.part + share_row_bytes(batch) / 4;
+  A.list = 0;
+  return hip(launch_shared(A, dtype, prefix_class(T, A.G, num_groups), many_rows(T, B), static_cast<hipStream_t>(stream)));
 }
 
 lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, const lora_heads_t* v,

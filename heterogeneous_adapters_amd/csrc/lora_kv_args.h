@@ -54,6 +54,7 @@ struct RopeArgs {
 };
 
 struct AttendArgs {
+  static constexpr bool kShared = false;
   Rows q, o;
   int32_t* counts;
   const int4* items;
@@ -64,6 +65,24 @@ struct AttendArgs {
   Cache cache;
   float scale_log2e;
   float* part;
+};
+
+struct ShareArgs {
+  const int32_t *group_indptr, *shared_len;
+  int32_t groups, B, T, G, hkv, prefix_class, item_cap, row_cap;
+  const int32_t *q_indptr, *kv_len, *positions;
+  int32_t *counts, *share, *cut, *first;
+  int4 *group_parts, *seq_parts, *items;
+};
+
+// Items of one list of a shared plan, or (list < 0) the join of their results.
+struct SharedArgs : AttendArgs {
+  static constexpr bool kShared = true;
+  const int32_t* share;
+  const int4* seq_parts;
+  const int32_t* token_seq;
+  float* part_ml;
+  int32_t groups, row_cap, list;
 };
 
 struct PromptArgs {
@@ -77,6 +96,8 @@ hipError_t launch_build(const BuildArgs& A, hipStream_t s);
 hipError_t launch_rope(const RopeArgs& A, int dtype, int blocks, hipStream_t s);
 hipError_t launch_gather(const RopeArgs& A, int dtype, int blocks, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& A, int dtype, bool many, hipStream_t s);
+hipError_t launch_share(const ShareArgs& A, hipStream_t s);
+hipError_t launch_shared(const SharedArgs& A, int dtype, int prefix_class, bool many, hipStream_t s);
 hipError_t launch_prompt(const PromptArgs& A, int dtype, int D, hipStream_t s);
 
 }  // namespace kv

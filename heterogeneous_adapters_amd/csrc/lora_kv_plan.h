@@ -94,5 +94,41 @@ LORA_KV_HD inline int last_row(int first, int rows, int len) {
 // -1 (not split)} and {first token row, rows of the request, position of its
 // first token, cached tokens}.
 
+// ---- shared plans: what the requests of a group have in common is attended to
+// by all of their rows together, the rest by each request, and both leave
+// partial results that a last launch joins.
+constexpr int kLists = 4;      // a shared plan's lists: 0 the groups' prefixes, 1 + c the requests' rests of class c
+constexpr int kShareItem = 3;  // int4 per item
+// Smallest chunk of a prefix, and the items (over all kv heads) that a plan
+// splits prefixes into.
+constexpr int kMinPrefixChunk = 512;
+constexpr int kTargetPrefix = 512;
+// counts of a shared plan: kLists item counts, then
+constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShareCheck = 8, kNumShare = 16;
+
+// Rows of a prefix's item, as a class, by the groups' average (the host's
+// arithmetic; sizes of single groups are known to the device only).
+LORA_KV_HD inline int prefix_class(int64_t T, int64_t G, int64_t groups) {
+  const int64_t rows = T * G;
+  return rows <= kUnit * groups ? 0 : rows <= kMidMost * groups ? 1 : 2;
+}
+// Most items of the prefix list: sum of tiles_g ceil(prefix_g / chunk) <=
+// kTargetPrefix / hkv + sum of tiles_g by the choice of the chunk.
+LORA_KV_HD inline int64_t prefix_cap(int64_t T, int64_t groups, int64_t hkv, int64_t G) {
+  return kTargetPrefix / hkv + 1 + T * G / rows_of_class(prefix_class(T, G, groups)) + 1 + groups;
+}
+LORA_KV_HD inline int64_t share_item_cap(int64_t T, int64_t B, int64_t groups, int64_t hkv, int64_t G) {
+  return item_cap(T, B, hkv, G) + groups;
+}
+// Most rows of partial results: a list's rows once, and as many again as the
+// rows of the items that its chunks add.
+LORA_KV_HD inline int64_t share_row_cap(int64_t T, int64_t hkv, int64_t G) {
+  return 2 * T * G + kWideRows * (kTargetPrefix / hkv + 1) + kMidRows * (kTargetItems / hkv + 1) +
+         kWideRows * (kTargetWide / hkv + 1);
+}
+LORA_KV_HD inline int32_t share_word(const int32_t* share) {
+  return check_word(share[kShareB], share[kShareT], share[0] + 7 * share[kShareGroups], share[1], share[2] + 5 * share[3], share[kShareRows]);
+}
+
 }  // namespace kv
 }  // namespace lora

@@ -24,12 +24,13 @@ ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 SCALING_NONE, SCALING_LINEAR, SCALING_NTK, SCALING_YARN, SCALING_BANDS = range(5)
 COUNT_TOKENS, COUNT_NEW_BLOCKS, COUNT_ITEMS, COUNT_PARTS, COUNT_CHUNK, COUNT_MID, COUNT_WIDE = range(7)
 COUNT_FLAGS = 8
-FLAG_LENGTH, FLAG_TOKENS, FLAG_FREE_LIST, FLAG_BLOCK_RANGE, FLAG_NONFINITE, FLAG_BATCH = 1, 2, 4, 8, 16, 32
+FLAG_LENGTH, FLAG_TOKENS, FLAG_FREE_LIST, FLAG_BLOCK_RANGE, FLAG_NONFINITE, FLAG_BATCH, FLAG_GROUPS = 1, 2, 4, 8, 16, 32, 64
 N_COUNTS = 16
 MAX_SEQS = 1 << 16
 EXPORTS = ("lora_kv_block_bytes", "lora_kv_batch_size", "lora_kv_batch_init", "lora_kv_build", "lora_rope_frequencies",
            "lora_rope", "lora_kv_append", "lora_kv_gather", "lora_kv_workspace_size", "lora_kv_attend",
-           "lora_prompt_attend")
+           "lora_kv_share_size", "lora_kv_share_init", "lora_kv_share", "lora_kv_share_workspace_size",
+           "lora_kv_attend_shared", "lora_prompt_attend")
 
 _vp, _i32, _i64, _f64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
 
@@ -47,6 +48,10 @@ class lora_kv_batch_t(ctypes.Structure):
     _fields_ = [("max_tokens", _i32), ("max_seqs", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32),
                 ("head_dim", _i32), ("q_indptr", _vp), ("kv_len", _vp), ("token_seq", _vp), ("positions", _vp),
                 ("slots", _vp), ("counts", _vp), ("plan", _vp)]
+
+
+class lora_kv_share_t(ctypes.Structure):
+    _fields_ = [("max_groups", _i32), ("counts", _vp), ("plan", _vp)]
 
 
 class lora_rope_t(ctypes.Structure):
@@ -72,6 +77,12 @@ def lib() -> dict:
             "lora_kv_gather": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _vp]),
             "lora_kv_workspace_size": (sz, [_vp]),
             "lora_kv_attend": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, ctypes.c_float, _vp, sz, _vp]),
+            "lora_kv_share_size": (sz, [_vp, _i32]),
+            "lora_kv_share_init": (_i32, [_vp, sz, _vp, _i32, _vp]),
+            "lora_kv_share": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
+            "lora_kv_share_workspace_size": (sz, [_vp, _vp]),
+            "lora_kv_attend_shared": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i32, _vp,
+                                             ctypes.c_float, _vp, sz, _vp]),
             "lora_prompt_attend": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_float, _vp]),
         }
         fns = {}
@@ -131,8 +142,9 @@ def _table(t: torch.Tensor):
     return at, stride, width
 
 
-def _call(name: str, stream, tensors, *args) -> None:
-    """The C call on the tensors' device and its current stream (or `stream`)."""
+def _call(name: str, stream, tensors, *args, fns=None) -> None:
+    """The C call (of `fns`, or this module's) on the tensors' device and its
+    current stream (or `stream`)."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t.get_device() != dev:
@@ -145,7 +157,7 @@ def _call(name: str, stream, tensors, *args) -> None:
         raise ValueError(f"{name}: a stream of {stream.device} for tensors on {tensors[0].device}")
     else:
         s = stream.cuda_stream
-    fn = (_bound or lib())[name]
+    fn = (fns or _bound or lib())[name]
     if _current() == dev:
         st = fn(*args, s)
     else:
@@ -245,6 +257,31 @@ def attend_workspace(batch: Batch) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=batch.buf.device)
 
 
+class Shared:
+    """Device buffer of a batch's shared plan, for up to max_groups groups of
+    requests that begin with the same cached tokens."""
+
+    def __init__(self, batch: Batch, max_groups: int):
+        L = lib()
+        n = L["lora_kv_share_size"](batch.ref, max_groups)
+        if n == 0:
+            raise ValueError("unsupported number of groups")
+        # zeroed, as a batch's buffer is
+        self.buf = torch.zeros(n, dtype=torch.uint8, device=batch.buf.device)
+        self.c = lora_kv_share_t()
+        self.ref = ctypes.addressof(self.c)
+        st = L["lora_kv_share_init"](self.buf.data_ptr(), n, batch.ref, max_groups, self.ref)
+        if st != 0:
+            raise lora.LoraError("lora_kv_share_init", st)
+        self.batch, self.groups = batch, 0
+
+
+def shared_workspace(batch: Batch, shared: Shared) -> torch.Tensor:
+    """Workspace of lora_kv_attend_shared (one serves every layer)."""
+    n = lib()["lora_kv_share_workspace_size"](batch.ref, shared.ref)
+    return torch.empty(n, dtype=torch.uint8, device=batch.buf.device)
+
+
 # ------------------------------------------------------- the C entry points
 def lora_rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = SCALING_NONE, factor: float = 1.0,
                           original: float = 0.0, low: float = 0.0, high: float = 0.0):
@@ -338,6 +375,35 @@ def lora_kv_attend(q: torch.Tensor, out: torch.Tensor, batch: Batch, block_table
     _call("lora_kv_attend", stream, (q, out, batch.buf, block_table, cache.data, ws),
           _heads(q, "q", batch.T, cache.head_dim, dtype), _heads(out, "out", batch.T, cache.head_dim, dtype), batch.T, batch.B,
           _code(dtype), batch.ref, table, stride, width, cache.ref, scale, ws.data_ptr(),
+          ws.numel() * ws.element_size())
+
+
+def lora_kv_share(group_indptr: torch.Tensor, shared_len: torch.Tensor, batch: Batch, shared: Shared, stream=None) -> None:
+    """Plan of a built batch whose requests group_indptr[g]..group_indptr[g+1]-1
+    begin with the same shared_len[g] cached tokens."""
+    groups = shared_len.shape[0]
+    if group_indptr.shape[0] != groups + 1:
+        raise ValueError("group_indptr has one entry more than shared_len")
+    if shared.batch is not batch:
+        raise ValueError("shared was made for another batch buffer")
+    _call("lora_kv_share", stream, (group_indptr, shared_len, batch.buf, shared.buf), _ints(group_indptr, "group_indptr"),
+          _ints(shared_len, "shared_len"), groups, batch.T, batch.B, batch.ref, shared.ref)
+    shared.groups = groups
+
+
+def lora_kv_attend_shared(q: torch.Tensor, out: torch.Tensor, batch: Batch, shared: Shared, block_table: torch.Tensor,
+                          cache: Cache, scale: float, ws: torch.Tensor, stream=None) -> None:
+    """lora_kv_attend, with the tokens that groups share attended to together."""
+    (table, stride, width), dtype = _table(block_table), q.dtype
+    if block_table.shape[0] != batch.B:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows, not {batch.B}")
+    if shared.batch is not batch:
+        raise ValueError("shared was made for another batch buffer")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _call("lora_kv_attend_shared", stream, (q, out, batch.buf, shared.buf, block_table, cache.data, ws),
+          _heads(q, "q", batch.T, cache.head_dim, dtype), _heads(out, "out", batch.T, cache.head_dim, dtype), batch.T, batch.B,
+          shared.groups, _code(dtype), batch.ref, shared.ref, table, stride, width, cache.ref, scale, ws.data_ptr(),
           ws.numel() * ws.element_size())
 
 

@@ -123,7 +123,8 @@ typedef struct {
 #define LORA_KV_FLAG_FREE_LIST 4  /* the free list ran out (slots of the rest are -1) */
 #define LORA_KV_FLAG_BLOCK_RANGE 8 /* a block id outside the cache (slot -1; not attended) */
 #define LORA_KV_FLAG_NONFINITE 16 /* lora_kv_append saw an infinity or NaN in K or V */
-#define LORA_KV_FLAG_BATCH 32     /* the batch was not built for this call's T and B */
+#define LORA_KV_FLAG_BATCH 32     /* the batch, or its shared plan, was not built for this call's T and B */
+#define LORA_KV_FLAG_GROUPS 64    /* lora_kv_share: a group outside the requests, or a negative length (not shared) */
 
 /* Bytes of the buffer (0 outside the limits: max_tokens in [0,
  * LORA_MAX_TOKENS], max_seqs in [1, LORA_KV_MAX_SEQS], num_q_heads a multiple
@@ -252,6 +253,58 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
                              const lora_kv_batch_t* batch, const int32_t* block_table, int64_t table_stride,
                              int32_t table_width, const lora_kv_cache_t* cache, float scale, void* ws,
                              size_t ws_bytes, void* stream);
+
+/* Requests that begin with the same cached tokens (a system prompt in front of
+ * an adapter's requests, a prompt that a search's beams have in common) attend
+ * to them together: what they share is read once for the rows of all of them,
+ * in place of once per request.
+ *
+ * A shared plan is carved from one caller buffer for a batch's capacity and
+ * for up to max_groups groups, built by lora_kv_share after each lora_kv_build
+ * and read by every layer's lora_kv_attend_shared.
+ * Sizes: 0 outside the limits (max_groups in [0, max_seqs]; 2 * max_tokens *
+ * query heads per kv head + 131072 < 2^31, and the work items of
+ * lora_kv_batch_size with max_groups more).
+ * Errors of init: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE. */
+typedef struct {
+  int32_t max_groups;
+  int32_t* counts; /* [16]: items of the prefixes and of the requests' three classes, rows of partial results, .. */
+  int32_t* plan;
+} lora_kv_share_t;
+size_t lora_kv_share_size(const lora_kv_batch_t* batch, int32_t max_groups);
+lora_status_t lora_kv_share_init(void* buf, size_t bytes, const lora_kv_batch_t* batch, int32_t max_groups,
+                                 lora_kv_share_t* out);
+
+/* Group g is the requests group_indptr[g] .. group_indptr[g+1]-1 (device,
+ * num_groups+1 entries, ascending within 0 .. B; requests before the first and
+ * behind the last group are in none), whose first shared_len[g] (device)
+ * tokens have the same K and V.  They are read through the table row of the
+ * group's first request that brings tokens; whether the other rows name the
+ * same blocks or copies of them does not matter.  What is attended to
+ * together is cut to a multiple of 16 tokens, and to what every row of the
+ * group sees of its own request (ctx_len, the shortest one's); the rest is
+ * attended to by each request.  A group that is empty, out of range or of
+ * negative length is not shared (LORA_KV_FLAG_GROUPS in the batch's flags for
+ * the last two).
+ * T, B: those of the batch's lora_kv_build.  No input may reach into the
+ * batch's or the plan's buffer.
+ * Errors: INVALID_ARG, WORKSPACE (past the capacity), HIP. */
+lora_status_t lora_kv_share(const int32_t* group_indptr, const int32_t* shared_len, int32_t num_groups, int32_t T,
+                            int32_t B, const lora_kv_batch_t* batch, const lora_kv_share_t* share, void* stream);
+
+/* lora_kv_attend with what groups share attended to together; the same result
+ * but for the order of its sums.  num_groups: that of lora_kv_share.
+ * ws: device, lora_kv_share_workspace_size(batch, share) bytes, 16-byte
+ * aligned, for partial results: calls that share it must not run at the same
+ * time.  A plan that was not built for this call's T, B and num_groups writes
+ * nothing (LORA_KV_FLAG_BATCH).
+ * Errors: as lora_kv_attend. */
+size_t lora_kv_share_workspace_size(const lora_kv_batch_t* batch, const lora_kv_share_t* share);
+lora_status_t lora_kv_attend_shared(const lora_heads_t* q, const lora_heads_t* o, int32_t T, int32_t B,
+                                    int32_t num_groups, int32_t dtype, const lora_kv_batch_t* batch,
+                                    const lora_kv_share_t* share, const int32_t* block_table, int64_t table_stride,
+                                    int32_t table_width, const lora_kv_cache_t* cache, float scale, void* ws,
+                                    size_t ws_bytes, void* stream);
 
 /* Causal attention of whole prompts over themselves: B prompts packed into T
  * token rows, prompt i in rows indptr[i] .. indptr[i+1]-1 (device, B+1
