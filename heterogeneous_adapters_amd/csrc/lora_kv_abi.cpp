@@ -473,7 +473,7 @@ lora_status_t lora_kv_share(const int32_t* group_indptr, const int32_t* shared_l
   A.T = T;
   A.hkv = batch->num_kv_heads;
   A.G = batch->num_q_heads / batch->num_kv_heads;
-  A.prefix_class = prefix_class(T, A.G, num_groups);
+  A.prefix_class = prefix_class(T, A.G, num_groups, batch->head_dim);
   A.item_cap = (int32_t)share_item_cap(batch->max_tokens, batch->max_seqs, share->max_groups, A.hkv, A.G);
   A.row_cap = (int32_t)share_row_cap(batch->max_tokens, A.hkv, A.G);
   A.q_indptr = batch->q_indptr;
@@ -526,7 +526,7 @@ lora_status_t lora_kv_attend_shared(const lora_heads_t* q, const lora_heads_t* o
   A.part = static_cast<float*>(ws);
   A.part_ml = A.part + share_row_bytes(batch) / 4;
   A.list = 0;
-  return hip(launch_shared(A, dtype, prefix_class(T, A.G, num_groups), many_rows(T, B), static_cast<hipStream_t>(stream)));
+  return hip(launch_shared(A, dtype, prefix_class(T, A.G, num_groups, batch->head_dim), many_rows(T, B), static_cast<hipStream_t>(stream)));
 }
 
 lora_status_t lora_prompt_attend(const lora_heads_t* q, const lora_heads_t* k, const lora_heads_t* v,

@@ -39,7 +39,8 @@ constexpr int kMidRows = 32, kWideRows = 128, kMidMost = 64;
 #define LORA_KV_HD
 #endif
 LORA_KV_HD inline bool many_rows(int32_t T, int32_t B) { return T > B; }
-LORA_KV_HD inline int rows_of_class(int c) { return c == 0 ? kUnit : c == 1 ? kMidRows : kWideRows; }
+constexpr int kPrefixRows = 256;  // class 3, of shared plans' prefixes only
+LORA_KV_HD inline int rows_of_class(int c) { return c == 0 ? kUnit : c == 1 ? kMidRows : c == 2 ? kWideRows : kPrefixRows; }
 
 LORA_KV_HD inline int32_t check_word(int32_t B, int32_t T, int32_t items, int32_t mid, int32_t wide, int32_t parts) {
   uint32_t h = 0x4b56u;
@@ -102,20 +103,20 @@ constexpr int kShareItem = 3;  // int4 per item
 // Smallest chunk of a prefix, and the items (over all kv heads) that a plan
 // splits prefixes into.
 constexpr int kMinPrefixChunk = 512;
-constexpr int kTargetPrefix = 512;
+constexpr int kTargetPrefix = 256;
 // counts of a shared plan: kLists item counts, then
 constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShareCheck = 8, kNumShare = 16;
 
 // Rows of a prefix's item, as a class, by the groups' average (the host's
 // arithmetic; sizes of single groups are known to the device only).
-LORA_KV_HD inline int prefix_class(int64_t T, int64_t G, int64_t groups) {
+LORA_KV_HD inline int prefix_class(int64_t T, int64_t G, int64_t groups, int head_dim) {
   const int64_t rows = T * G;
-  return rows <= kUnit * groups ? 0 : rows <= kMidMost * groups ? 1 : 2;
+  return rows <= kUnit * groups ? 0 : rows <= kMidMost * groups ? 1 : rows <= kWideRows * groups || head_dim > 128 ? 2 : 3;
 }
 // Most items of the prefix list: sum of tiles_g ceil(prefix_g / chunk) <=
 // kTargetPrefix / hkv + sum of tiles_g by the choice of the chunk.
-LORA_KV_HD inline int64_t prefix_cap(int64_t T, int64_t groups, int64_t hkv, int64_t G) {
-  return kTargetPrefix / hkv + 1 + T * G / rows_of_class(prefix_class(T, G, groups)) + 1 + groups;
+LORA_KV_HD inline int64_t prefix_cap(int cls, int64_t T, int64_t groups, int64_t hkv, int64_t G) {
+  return kTargetPrefix / hkv + 1 + T * G / rows_of_class(cls) + 1 + groups;
 }
 LORA_KV_HD inline int64_t share_item_cap(int64_t T, int64_t B, int64_t groups, int64_t hkv, int64_t G) {
   return item_cap(T, B, hkv, G) + groups;
@@ -123,7 +124,7 @@ LORA_KV_HD inline int64_t share_item_cap(int64_t T, int64_t B, int64_t groups, i
 // Most rows of partial results: a list's rows once, and as many again as the
 // rows of the items that its chunks add.
 LORA_KV_HD inline int64_t share_row_cap(int64_t T, int64_t hkv, int64_t G) {
-  return 2 * T * G + kWideRows * (kTargetPrefix / hkv + 1) + kMidRows * (kTargetItems / hkv + 1) +
+  return 2 * T * G + kPrefixRows * (kTargetPrefix / hkv + 1) + kMidRows * (kTargetItems / hkv + 1) +
          kWideRows * (kTargetWide / hkv + 1);
 }
 LORA_KV_HD inline int32_t share_word(const int32_t* share) {

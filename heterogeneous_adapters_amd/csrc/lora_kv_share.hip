@@ -9,6 +9,8 @@
 // converted once per tile of rows in place of once per request, and becomes a
 // matrix product.  The second is lora_kv_attend's work over what is left.
 // Either is cut into chunks that leave partial results; one launch joins them.
+#include <utility>
+
 #include "lora_kv_scan.h"
 #include "lora_kv_tile.h"
 
@@ -18,6 +20,16 @@ namespace kv {
 namespace {
 
 constexpr int kPlanThreads = 512;
+
+// f of 0, 1, .. N-1 as constants.
+template <int... I, class F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+  each_of(std::make_integer_sequence<int, N>(), f);
+}
 
 // The group of request i, or -1.
 __device__ __forceinline__ int group_of(const ShareArgs& A, int i) {
@@ -192,6 +204,277 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
   }
 }
 
+// ------------------------------------------------------- prefixes of many rows
+// 256 rows on a prefix's keys, which have no limits by row: eight waves of 32
+// rows share the conversion of 64 keys at a time to bf16 in LDS (four waves
+// convert K, four V, a unit of 16 tokens each). The products of a tile run
+// between the softmax of another: while a wave's weights of tile t are formed,
+// the matrix unit has the weights of tile t-1 times V and S of tile t+1.
+template <int NC>
+__global__ __launch_bounds__(512, 2) void prefix_kernel(const SharedArgs A) {
+  constexpr int D = 32 * NC, kKeys = 64;
+  constexpr int kSteps = D / 16, kDims = D / 32;
+  // Rows of LDS, 16 bytes longer than their values: 16 lanes reading 16 bytes
+  // of a row each meet all 64 banks, and one register addresses them all.
+  constexpr int kRowK = 2 * D + 16, kRowV = 2 * kKeys + 16;
+  __shared__ __attribute__((aligned(128))) uint8_t s_k[2][kKeys * kRowK], s_v[2][D * kRowV];
+  __shared__ __attribute__((aligned(4))) uint8_t s_bad[4][4];  // by tile: its units that no row sees
+  const int hkv = A.cache.heads;
+  const int item = blockIdx.x / hkv, kvh = blockIdx.x - item * hkv;
+  Item it;
+  if (!read_item(A, 3, 0, item, 0, kPrefixRows, it)) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
+  const int m16 = lane & 15, g = lane >> 4;
+  const int G = A.G, row_first = it.row0 + wave * 32;
+
+  bf16x8 qf[kSteps];
+  {
+    const int row = min(row_first + n, it.nrows - 1), jq = row / G;
+    const uint16_t* q = static_cast<const uint16_t*>(A.q.p) + (int64_t)(it.qs + jq) * A.q.ts + (kvh * G + row - jq * G) * A.q.hs;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(q + 16 * s + 8 * h);
+  }
+
+  const int32_t* trow = A.table + (int64_t)it.seq * A.tstride;
+  const uint8_t* head = A.cache.base + ((int64_t)kvh << A.cache.bt_log2 >> 4) * (544 * NC);
+  const int unit_mask = (1 << (A.cache.bt_log2 - 4)) - 1;
+  const int n_tiles = (it.end - it.begin + kKeys - 1) / kKeys;
+  bool bad_block = false;
+
+  const bool is_v = wave >= 4;  // this wave converts V of its unit, or K
+  const int first = it.begin + kUnit * (wave & 3);  // its unit's first token in tile 0
+  // Block ids of this wave's unit in 64 tiles, one per lane; -1 outside the cache.
+  auto fetch_ids = [&](int tile) {
+    const int token = first + (tile + lane) * kKeys;
+    int id = 0;
+    if (token < it.end) {
+      const int at = token >> A.cache.bt_log2;
+      id = at < A.width ? trow[at] : -1;  // a table of another call may be narrower
+      if ((unsigned)id >= (unsigned)A.cache.blocks) id = -1, bad_block = true;
+    }
+    return id;
+  };
+  uint32_t code[NC], scale[NC];  // a lane's share of the unit's K or V (of K's scales the first bytes)
+  int id = 0, ids = fetch_ids(0);
+  auto load = [&](int tile) {
+    if (tile && tile % 64 == 0) ids = fetch_ids(tile);
+    id = __builtin_amdgcn_readlane(ids, tile % 64);
+    // behind the last token: the id is 0, a block of the cache
+    const uint8_t* rec = head + max(id, 0) * A.cache.stride + (((first + tile * kKeys) >> 4) & unit_mask) * (544 * NC);
+    if (is_v) {
+      __builtin_memcpy(code, __builtin_assume_aligned(rec + 256 * NC + (g * 16 + m16) * 4 * NC, 4), 4 * NC);
+      __builtin_memcpy(scale, __builtin_assume_aligned(rec + 528 * NC + 4 * g * NC, 4), 4 * NC);
+    } else {
+      __builtin_memcpy(code, __builtin_assume_aligned(rec + (m16 * 4 + g) * 4 * NC, 4), 4 * NC);
+      __builtin_memcpy(scale, rec + 512 * NC + m16 * NC, NC);
+    }
+  };
+  const int k_to = (kUnit * (wave & 3) + m16) * kRowK + g * 16;
+  // tokens 4g..4g+3 of the unit, one dim: 8 bytes; the two halves of a 16-byte
+  // piece are the tokens 8 apart that one lane of P holds
+  const int v_to = m16 * kRowV + (2 * (wave & 3) + (g & 1)) * 16 + (g >> 1) * 8;
+  // A unit outside the cache, or behind the last token: its bytes may hold
+  // anything, a scale of NaN among it.
+  auto convert_k = [&](int tile, int buf) {
+    if (lane == 0) s_bad[tile & 3][wave] = id < 0 || first + tile * kKeys >= it.end;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float sc = byte_scale(scale[c >> 2], c & 3);
+      *reinterpret_cast<u32x4*>(s_k[buf] + k_to + 64 * c) =
+          u32x4{fp4_pair(code[c], sc, 0), fp4_pair(code[c], sc, 1), fp4_pair(code[c], sc, 2), fp4_pair(code[c], sc, 3)};
+    }
+  };
+  auto convert_v = [&](int tile, int buf) {
+    if (id < 0 || first + tile * kKeys >= it.end) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) code[c] = scale[c] = 0;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      uint32_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = j * NC + c;
+        r[j] = fp4_pair(code[c], byte_scale(scale[at >> 2], at & 3), j);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t sel = e ? 0x07060302u : 0x05040100u;
+        *reinterpret_cast<uint2*>(s_v[buf] + v_to + (32 * c + 16 * e) * kRowV) =
+            make_uint2(__builtin_amdgcn_perm(r[1], r[0], sel), __builtin_amdgcn_perm(r[3], r[2], sel));
+      }
+    }
+  };
+
+  // The x-th piece of a turn's products: V's first, whose weights' registers
+  // then are free for this turn's, K's when half of this turn's scores are.
+  constexpr int kHalf = 4 * NC;
+  auto piece_of = [&](int x, int buf) {
+    if (x < kHalf) {
+      const int c = x / kDims, d = x % kDims;
+      return *reinterpret_cast<const bf16x8*>(s_v[buf] + (n + 32 * d) * kRowV + (2 * c + h) * 16);
+    }
+    const int u = (x - kHalf) / kSteps, c = (x - kHalf) % kSteps;
+    return *reinterpret_cast<const bf16x8*>(s_k[buf] + (n + 32 * u) * kRowK + (2 * c + h) * 16);
+  };
+
+  f16v o[kDims], s[2];
+  float m = kNone, l = 0.0f, most;
+  bool far = false;  // some row's scores are
+  bf16x8 pf[4];      // the weights of the tile before
+#pragma unroll
+  for (int d = 0; d < kDims; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  auto highest = [&](int u) {  // .. of the first 32 tokens' scores, and of the others
+    if (u == 0) most = s[0][0];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, s[u][i]);
+  };
+
+  // Tile t's weights, next to the products of its neighbours; t's parity is
+  // `which`.  `most` holds the highest of its first 32 tokens' scores.
+  auto turn = [&](int t, auto which, auto first) {
+    constexpr int buf = which;
+    constexpr bool kFirst = first;
+    constexpr int kFrom = kFirst ? kHalf : 0, kSlots = 2 * kHalf - kFrom, kAhead = 4;
+    bf16x8 ahead[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) ahead[x] = piece_of(kFrom + x, 1 - buf);
+    const uint32_t bad = (uint32_t)uniform((int)*reinterpret_cast<const uint32_t*>(s_bad[t & 3]));
+    if (bad) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if ((bad >> (8 * (2 * u + (i >> 3)))) & 1) s[u][i] = -INFINITY;
+      highest(0);
+    }
+    highest(1);
+    float alpha = 1.0f;
+    const bool moved = __any(most * A.scale_log2e > m + kSlack);
+    if (moved) {
+      const float mn = fmaxf(m, fmaxf(most, __shfl_xor(most, 32)) * A.scale_log2e);
+      alpha = exp2_hw(m - mn);
+      m = mn;
+      far = far || __any(is_far(mn));
+      l *= alpha;
+    }
+    float by = A.scale_log2e, less = m;
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = far_exponent(s[i >> 4][i & 15], by, less);
+      by = 1.0f, less = 0.0f;
+    }
+    if (is_v) {
+      convert_v(t, buf);
+      load(t + 1);
+    } else {
+      convert_k(t + 2, buf);
+      load(t + 3);
+    }
+
+    f16v next[2];
+    bf16x8 now[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) next[u][i] = 0.0f;
+    constexpr int kMaxFrom = kSlots - 2 * NC + 1, kPer = 2 * NC - 1;
+    // one product a slot, in this order
+    each<kSlots>([&](auto slot) {
+      constexpr int y = slot, x = kFrom + y;
+      __builtin_amdgcn_sched_barrier(0);
+      const bf16x8 a = ahead[y % kAhead];
+      if constexpr (x < kHalf) {
+        o[x % kDims] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pf[x / kDims], o[x % kDims], 0, 0, 0);
+      } else {
+        constexpr int u = (x - kHalf) / kSteps, c = (x - kHalf) % kSteps;
+        next[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[c], next[u], 0, 0, 0);
+      }
+      if constexpr (y + kAhead < kSlots) ahead[y % kAhead] = piece_of(x + kAhead, 1 - buf);
+      // this tile's weights
+      constexpr int from = y * 32 / kSlots, to = (y + 1) * 32 / kSlots;
+      each<to - from>([&](auto at) {
+        constexpr int i = from + at;
+        now[i >> 3][i & 7] = (__bf16)exp2_hw(fmaf(s[i >> 4][i & 15], by, -less));
+        if constexpr ((i & 7) == 7) l = add8(now[i >> 3], l);
+      });
+      if constexpr (y >= kMaxFrom) {  // the next tile's first scores
+        constexpr int a0 = (y - kMaxFrom) * 16 / kPer, a1 = (y - kMaxFrom + 1) * 16 / kPer;
+        each<a1 - a0>([&](auto at) {
+          constexpr int i = a0 + at;
+          most = i ? fmaxf(most, next[0][i]) : next[0][0];
+        });
+      }
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    // formed here, not where they are used
+#pragma unroll
+    for (int c = 0; c < 4; ++c) asm volatile("" : "+v"(now[c]));
+    asm volatile("" : "+v"(most));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) s[u] = next[u];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) pf[c] = now[c];
+    if (moved) {
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[d] *= alpha;
+    }
+    __syncthreads();  // K of t+2 and V of t are in LDS, and what this turn read is free
+  };
+
+  const std::integral_constant<int, 0> zero;
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<bool, true> yes;
+  const std::integral_constant<bool, false> no;
+  load(0);
+  if (!is_v) {
+    convert_k(0, 0);
+    load(1);
+    convert_k(1, 1);
+    load(2);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(piece_of(kHalf + u * kSteps + c, 0), qf[c], s[u], 0, 0, 0);
+  }
+  highest(0);
+  __syncthreads();  // turn 0 writes K of tile 2 there
+  turn(0, zero, yes);
+  int t = 1;
+  for (; t + 1 < n_tiles; t += 2) {
+    turn(t, one, no);
+    turn(t + 1, zero, no);
+  }
+  auto finish = [&](auto which) {  // O of the last tile
+    constexpr int buf = which;
+#pragma unroll
+    for (int x = 0; x < kHalf; ++x)
+      o[x % kDims] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(piece_of(x, buf), pf[x / kDims], o[x % kDims], 0, 0, 0);
+  };
+  if (t < n_tiles) {
+    turn(t, one, no);
+    finish(one);
+  } else {
+    finish(zero);
+  }
+  if (__any(bad_block) && lane == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BLOCK_RANGE);
+
+  l += __shfl_xor(l, 32);
+  if (row_first + n < it.nrows) {
+#pragma unroll
+    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        store_part<D>(A, it, kvh, wave * 32 + n, 32 * d + 2 * i + 4 * h, f4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]}, m, l);
+  }
+}
+
 // Four dims of a row per thread.
 template <class E>
 __global__ __launch_bounds__(256) void join_kernel(const SharedArgs A, int vecs) {
@@ -241,16 +524,25 @@ hipError_t launch(SharedArgs A, int prefix_cls, bool many, hipStream_t s) {
   auto run = [&](int list, int cls, int64_t items) {
     A.list = list;
     const unsigned n = (unsigned)(items * hkv);
+    if constexpr (sizeof(typename E::T) == 2) {
+      if constexpr (NC <= 4) {
+        if (list == 0 && cls == 3) {
+          prefix_kernel<NC><<<n, 512, 0, s>>>(A);
+          return;
+        }
+      }
+    }
     if (cls == 0) {
       attend_kernel<E, NC, 1, 0, SharedArgs><<<n, 64 * kWaves, 0, s>>>(A);
     } else if (cls == 1) {
       attend_kernel<E, NC, 2, 1, SharedArgs><<<n, 64 * kWaves, 0, s>>>(A);
     } else {
       if constexpr (sizeof(typename E::T) == 2) attend_wide_kernel<NC, SharedArgs><<<n, 256, 0, s>>>(A);
-      else attend_kernel<E, NC, 2, 2, SharedArgs><<<n * (kWideRows / kMidRows), 64 * kWaves, 0, s>>>(A);
+      else if (cls == 2) attend_kernel<E, NC, 2, 2, SharedArgs><<<n * (kWideRows / kMidRows), 64 * kWaves, 0, s>>>(A);
+      else attend_kernel<E, NC, 2, 3, SharedArgs><<<n * (kPrefixRows / kMidRows), 64 * kWaves, 0, s>>>(A);
     }
   };
-  if (A.groups > 0) run(0, prefix_cls, prefix_cap(A.T, A.groups, hkv, A.G));
+  if (A.groups > 0) run(0, prefix_cls, prefix_cap(prefix_cls, A.T, A.groups, hkv, A.G));
   for (int c = many ? 2 : 0; c >= 0; --c) run(1 + c, c, class_cap(c, A.T, A.B, hkv, A.G));
   const int vecs = 8 * NC;
   const int64_t tasks = (int64_t)A.T * hkv * A.G * vecs;

@@ -258,7 +258,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && NC <= 4 && sizeof(typename 
   constexpr int W = kWaves, kThreads = 64 * W;
   constexpr int NS = sizeof(typename E::T) == 2 ? 1 : 3;
   constexpr int D = 32 * NC, LD = D + 4, kVecs = D / 4;
-  constexpr int kPieces = CLS == 2 ? kWideRows / (kUnit * RT) : 1, kUnits = RT * kPieces;
+  constexpr int kPieces = CLS >= 2 ? (CLS == 2 ? kWideRows : kPrefixRows) / (kUnit * RT) : 1, kUnits = RT * kPieces;
   typedef typename E::T T;
   __shared__ float s_o[W][kUnit][LD];
   __shared__ float s_m[W][kUnit], s_l[W][kUnit];
