@@ -13,7 +13,7 @@ namespace beam {
 constexpr int kChunk = 2048;  // logits that a wave holds at once, 32 per lane
 // Waves that a selection's rows are cut into, where the vocabulary has as many
 // chunks.
-constexpr int kTargetWaves = 8192;
+constexpr int kTargetWaves = 4096;
 
 // Chunks of a row: its first logit may lie anywhere in a 16-byte vector.
 inline int64_t row_chunks(int64_t vocab) { return (vocab + 7 + kChunk - 1) / kChunk; }

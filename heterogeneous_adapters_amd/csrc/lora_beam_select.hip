@@ -9,6 +9,8 @@
 // by the lower token).  A chunk whose highest logit is below the last of these
 // is done with its sum.  A second launch joins the waves of each row and ranks the request's
 // beams * beams candidates in 64 bits.
+#include <type_traits>
+
 #include "lora_beam_args.h"
 #include "lora_kv_dev.h"
 
@@ -22,9 +24,11 @@ namespace {
 constexpr float kLog2eHi = 1.44269502162933349609375f;  // log2(e) to 24 bits, and the rest
 constexpr float kLog2eLo = 1.92596299112661746887e-08f;
 
-// e^d for d <= 0, -inf among them: off by the rounding of d log2(e), 2^-24 of
-// it either way, and of exp2.
-__device__ __forceinline__ float exp_of(float d) { return exp2_hw(fmaf(d, kLog2eLo, d * kLog2eHi)); }
+constexpr double kLog2e = 1.44269504088896340736, kLn2 = 0.693147180559945309417;
+constexpr float kSlackLogit = 8.0f;
+
+// Logits past this leave fp32's range times log2(e).
+constexpr float kFarLogit = 1e38f;
 
 // Floats as integers of the same order; 0 is below every one that stands for a logit.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -36,12 +40,21 @@ __device__ __forceinline__ float from_ordered(uint32_t k) {
 }
 constexpr uint32_t kMinusInf = 0x007fffffu;  // ordered(-inf)
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t x, int lane) {
-  return (uint64_t)(uint32_t)__shfl((int)(uint32_t)x, lane) | (uint64_t)(uint32_t)__shfl((int)(x >> 32), lane) << 32;
+// The lane before's, 0 in the first.
+__device__ __forceinline__ uint64_t shift64(uint64_t x) {
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, 0x138, 0xf, 0xf, true);  // wave_shr:1
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), 0x138, 0xf, 0xf, true);
+  return (uint64_t)(uint32_t)lo | (uint64_t)(uint32_t)hi << 32;
 }
 __device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {  // a uniform lane
   return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane) |
          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32;
+}
+
+// A value sent to lane `to` of each lane; 0 where none is sent.
+__device__ __forceinline__ uint64_t send64(uint64_t x, int to) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_ds_permute(4 * to, (int)(uint32_t)x) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_ds_permute(4 * to, (int)(x >> 32)) << 32;
 }
 
 // The highest n keys seen so far, lane i the i-th; 0 where there are none.
@@ -50,16 +63,34 @@ struct Best {
   __device__ __forceinline__ void put(uint64_t key, int n) {  // a uniform key above `least`
     const int lane = threadIdx.x & 63;
     const int at = __popcll(__ballot(list > key));
-    const uint64_t up = shfl64(list, max(lane - 1, 0));
+    const uint64_t up = shift64(list);
     list = lane < at ? list : lane == at ? key : up;
+    least = lane64(list, n - 1);
+  }
+  // The keys of the first `count` lanes (of others 0), all different: each
+  // finds its place by counting those above it.
+  __device__ __forceinline__ void merge(uint64_t keys, int count, int n) {
+    const int lane = threadIdx.x & 63;
+    int mine = lane, place = 0;  // of `list`, of `keys`
+    for (int j = 0; j < count; ++j) {
+      const uint64_t k = lane64(keys, j);
+      mine += k > list;
+      place += k > keys;
+    }
+    if (least || lane64(list, 0)) {
+      for (int j = 0; j < n; ++j) place += lane64(list, j) > keys;
+    }
+    // no list has a 64th entry: what has no place goes there
+    const uint64_t a = send64(list, list && mine < n ? mine : 63), b = send64(keys, keys && place < n ? place : 63);
+    list = lane < n ? a | b : 0;
     least = lane64(list, n - 1);
   }
 };
 
-// The n-th highest of the lanes' values.
+// The n-th highest of the lanes' values, or a little less: its upper 16 bits.
 __device__ __forceinline__ uint32_t nth_highest(uint32_t x, int n) {
   uint32_t t = 0;
-  for (int b = 31; b >= 0; --b) {
+  for (int b = 31; b >= 16; --b) {
     const uint32_t up = t | 1u << b;
     if (__popcll(__ballot(x >= up)) >= n) t = up;
   }
@@ -70,7 +101,9 @@ template <class E>
 __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
   typedef typename E::T T;
   constexpr int kEpv = E::kEpv, kVecs = 32 / kEpv;
+  __shared__ uint64_t s_cand[4][64];
   const int lane = threadIdx.x & 63;
+  uint64_t* cand = s_cand[threadIdx.x >> 6];
   const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int row = uniform((int)(job / A.waves)), wave = uniform((int)(job - (int64_t)row * A.waves));
   if (row >= A.requests * A.beams) return;
@@ -83,8 +116,11 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
   const int first = wave * A.chunks, last = min(first + A.chunks, (A.vocab + skew + kChunk - 1) / kChunk);
 
   Best best;
-  float ref = -INFINITY;  // the highest logit so far
+  float ref = -INFINITY;  // a logit that the others pass by 8 at most
+  float less = 0.0f;      // ref log2(e)
+  double by = 0.0;        // what its rounding makes of each weight
   double sum = 0.0;       // of e^(x - ref), this lane's share
+  float bound = -INFINITY;  // logits below this are not among the highest
   bool odd = false;
   u32x4 raw[kVecs] = {};
   auto vec_at = [&](int chunk, int v) { return chunk * kChunk + (v * 64 + lane) * kEpv - skew; };
@@ -115,45 +151,87 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
         for (int i = 0; i < kEpv; ++i) y[v * kEpv + i] = at + i >= 0 && at + i < A.vocab ? to_f(x[at + i]) : -INFINITY;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (!(y[i] < INFINITY)) odd = true, y[i] = -INFINITY;
 
-    float most = y[0];
+    float most, s;
+    auto weigh = [&](auto rare) {
+      most = y[0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) most = fmaxf(most, y[i]);
-    float top = most;
+      for (int i = 1; i < 32; ++i) most = fmaxf(most, y[i]);
+      float top = most;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if (top == -INFINITY) continue;
-    if (top > ref) {
-      sum *= exp((double)ref - (double)top);  // 0 at first
-      ref = top;
+      for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+      if (top > ref + kSlackLogit) {
+        if (ref > -INFINITY) sum *= exp((double)ref - (double)top);
+        ref = top;
+        less = ref * kLog2eHi;
+        const double off = ((double)less - (double)ref * kLog2e) * kLn2;  // 2^-24 of it: e^off by its first terms
+        by = 1.0 + off * (1.0 + 0.5 * off);
+      }
+      s = 0.0f;
+      if (rare) {
+        if (ref == -INFINITY) return;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += exp2_hw(fmaf(y[i] - ref, kLog2eLo, (y[i] - ref) * kLog2eHi));
+        sum += (double)s;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += exp2_hw(fmaf(y[i], kLog2eLo, fmaf(y[i], kLog2eHi, -less)));
+      }
+    };
+    const double sum0 = sum, by0 = by;
+    const float ref0 = ref, less0 = less;
+    weigh(std::false_type());
+    // A NaN, an infinity or a logit that is far shows in the sum or the highest.
+    if (__any(!(s == s)) || !(fabsf(ref) < kFarLogit)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!(y[i] < INFINITY)) odd = true, y[i] = -INFINITY;
+      sum = sum0, by = by0, ref = ref0, less = less0;
+      weigh(std::true_type());
+    } else {
+      sum += (double)s * by;
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s += exp_of(y[i] - ref);
-    sum += (double)s;
 
     // candidates
-    uint32_t bound = (uint32_t)(best.least >> 32);
-    const uint32_t high = ordered(most + 0.0f);
-    if (!__any(high >= bound)) continue;
-    if (bound == 0) bound = max(nth_highest(high, A.beams), kMinusInf + 1);
+    if (!__any(most >= bound) || !__any(most > -INFINITY)) continue;
+    // token and key of this lane's i-th logit, for any lane's bits
+    auto key_of = [&](int i, uint32_t bits, int from) {
+      const int token = chunk * kChunk + ((i / kEpv) * 64 + from) * kEpv + i % kEpv - skew;
+      return (uint64_t)ordered(__uint_as_float(bits) + 0.0f) << 32 | (uint32_t)~token;  // one zero
+    };
+    if (best.least == 0) {  // the first chunk: sorted together
+      const uint32_t nth = nth_highest(ordered(most), A.beams);
+      bound = fmaxf(bound, nth > kMinusInf ? from_ordered(nth) : -3.402823466e38f);
+      int count = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t k = ordered(y[i] + 0.0f);  // one zero
-      uint64_t mask = __ballot(k >= bound);
-      while (mask) {
-        const int from = __ffsll((long long)mask) - 1;
-        mask &= mask - 1;
-        const int token = chunk * kChunk + ((i / kEpv) * 64 + from) * kEpv + i % kEpv - skew;
-        const uint64_t key = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)k, from) << 32 | (uint32_t)~token;
-        if (key > best.least) {
-          best.put(key, A.beams);
-          bound = max(bound, (uint32_t)(best.least >> 32));
+      for (int i = 0; i < 32; ++i) {
+        const uint64_t mask = __ballot(y[i] >= bound);
+        const int at = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (y[i] >= bound && at < 64) cand[at] = key_of(i, __float_as_uint(y[i]), lane);
+        count += __popcll(mask);
+      }
+      if (count <= 64) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        best.merge(lane < count ? cand[lane] : 0, count, A.beams);
+        if (best.least) bound = fmaxf(bound, from_ordered((uint32_t)(best.least >> 32)));
+        continue;
+      }
+    }
+    // few, or many equal ones: one after the other
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      if (!(__ballot(y[j] >= bound) | __ballot(y[j + 1] >= bound) | __ballot(y[j + 2] >= bound) | __ballot(y[j + 3] >= bound))) continue;
+#pragma unroll
+      for (int i = j; i < j + 4; ++i) {
+        uint64_t mask = __ballot(y[i] >= bound);
+        while (mask) {
+          const int from = __ffsll((long long)mask) - 1;
+          mask &= mask - 1;
+          const uint64_t key = key_of(i, (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(y[i]), from), from);
+          if (key > best.least) best.put(key, A.beams);
         }
       }
+      if (best.least) bound = fmaxf(bound, from_ordered((uint32_t)(best.least >> 32)));
     }
   }
   if (__any(odd) && lane == 0 && A.flags) atomicOr(A.flags, LORA_BEAM_FLAG_LOGITS);
@@ -164,15 +242,15 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
   if (lane == 0) A.sums[2 * at] = ref, A.sums[2 * at + 1] = sum;
 }
 
-// One work-group per request.
-__global__ __launch_bounds__(256) void pick_kernel(const SelectArgs A) {
+// One work-group per request, a wave per row where there are as many.
+__global__ __launch_bounds__(1024) void pick_kernel(const SelectArgs A) {
   constexpr int kMost = LORA_BEAM_MAX;
   __shared__ double s_rank[kMost * kMost], s_total[kMost * kMost];
   __shared__ int32_t s_token[kMost * kMost];
   __shared__ float s_score[kMost];
   __shared__ int32_t s_length[kMost], s_done[kMost], s_chosen;
   const int W = A.beams, row0 = blockIdx.x * W;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   if (threadIdx.x < W) {
     s_score[threadIdx.x] = A.score[row0 + threadIdx.x];
     s_length[threadIdx.x] = A.length[row0 + threadIdx.x];
@@ -180,7 +258,7 @@ __global__ __launch_bounds__(256) void pick_kernel(const SelectArgs A) {
   }
   if (threadIdx.x == 0) s_chosen = 0;
   __syncthreads();
-  for (int w = wave; w < W; w += 4) {
+  for (int w = wave; w < W; w += waves) {
     const float score = s_score[w];
     const bool live = fabsf(score) < INFINITY, done = s_done[w] != 0;
     double total = -INFINITY;
@@ -204,13 +282,7 @@ __global__ __launch_bounds__(256) void pick_kernel(const SelectArgs A) {
       const int keys = A.waves * W;
       for (int i0 = 0; i0 < keys; i0 += 64) {
         const uint64_t key = i0 + lane < keys ? A.keys[at * W + i0 + lane] : 0;
-        uint64_t mask = __ballot(key > best.least);
-        while (mask) {
-          const int from = __ffsll((long long)mask) - 1;
-          mask &= mask - 1;
-          const uint64_t k = lane64(key, from);
-          if (k > best.least) best.put(k, W);
-        }
+        best.merge(key, min(keys - i0, 64), W);
       }
       if (lane < W && best.list) {
         total = (double)score + ((double)from_ordered((uint32_t)(best.list >> 32)) - ref - log(sum));
@@ -224,19 +296,28 @@ __global__ __launch_bounds__(256) void pick_kernel(const SelectArgs A) {
     }
   }
   __syncthreads();
-  // each candidate's place: those of a row lie in their order
-  const int all = W * W;
-  for (int i = threadIdx.x; i < all; i += 256) {
+  // each candidate's place: a row's lie in their order, so of another row's the
+  // better ones are counted by halving; four threads count for one
+  const int all = W * W, part = threadIdx.x & 3;
+  for (int i = threadIdx.x >> 2; i < all; i += blockDim.x >> 2) {
     const double rank = s_rank[i];
-    if (!(s_total[i] > -INFINITY)) continue;
-    int before = 0;
-    for (int j = 0; j < all; ++j) {
-      const double other = s_rank[j];
-      before += s_total[j] > -INFINITY && (other > rank || (other == rank && j < i));
+    const int w = i / W;
+    int before = part ? 0 : i - w * W;
+    for (int o = part; o < W && before < W; o += 4) {
+      if (o == w) continue;
+      int lo = 0, hi = W;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const double other = s_rank[o * W + mid];
+        if (other > rank || (other == rank && o < w)) lo = mid + 1; else hi = mid;
+      }
+      before += lo;
     }
-    if (before >= W) continue;
+    before += __shfl_xor(before, 1);
+    before += __shfl_xor(before, 2);
+    if (part || before >= W || !(s_total[i] > -INFINITY)) continue;
     atomicAdd(&s_chosen, 1);
-    const int w = i / W, to = row0 + before, token = s_token[i];
+    const int to = row0 + before, token = s_token[i];
     const bool done = s_done[w] != 0;
     A.parent[to] = row0 + w;
     A.token[to] = token;
@@ -262,7 +343,7 @@ hipError_t launch_select(const SelectArgs& A, int dtype, hipStream_t s) {
   const unsigned blocks = (unsigned)((jobs + 3) / 4);
   if (dtype == LORA_DTYPE_BF16) rows_kernel<Bf16><<<blocks, 256, 0, s>>>(A);
   else rows_kernel<F32><<<blocks, 256, 0, s>>>(A);
-  pick_kernel<<<A.requests, 256, 0, s>>>(A);
+  pick_kernel<<<A.requests, 64 * max_i(4, min_i(A.beams, 16)), 0, s>>>(A);
   return hipGetLastError();
 }
 
