@@ -16,7 +16,7 @@ import torch
 
 from . import kv, lora
 
-MAX_BEAMS, MAX_VOCAB, MAX_LAYERS = 32, 1 << 24, 1024
+MAX_BEAMS, MAX_VOCAB, MAX_LAYERS, MAX_PENALTY = 32, 1 << 24, 1024, 16
 FLAG_LOGITS, FLAG_PARENT, FLAG_LENGTH, FLAG_FREE_LIST, FLAG_BLOCK_RANGE = 1, 2, 4, 8, 16
 COUNT_COPIES, COUNT_FREED, COUNT_FLAGS = 0, 1, 8
 N_COUNTS = 16

@@ -78,7 +78,7 @@ lora_status_t lora_beam_select(const void* logits, int64_t row_stride, int32_t d
                                int32_t beams, int32_t vocab, const lora_beams_t* in, float length_penalty, int32_t eos,
                                int32_t* parent, int32_t* token, const lora_beams_t* out, int32_t* flags, void* ws,
                                size_t ws_bytes, void* stream) {
-  if (num_requests < 0 || beams < 1 || vocab < 1 || !in || !out || !isfinite(length_penalty) || eos < -1 || eos >= vocab)
+  if (num_requests < 0 || beams < 1 || vocab < 1 || !in || !out || !(fabsf(length_penalty) <= LORA_BEAM_MAX_PENALTY) || eos < -1 || eos >= vocab)
     return LORA_ERR_INVALID_ARG;
   if (dtype != LORA_DTYPE_BF16 && dtype != LORA_DTYPE_F32) return LORA_ERR_UNSUPPORTED;
   if (!select_ok(num_requests, beams, vocab)) return LORA_ERR_UNSUPPORTED;

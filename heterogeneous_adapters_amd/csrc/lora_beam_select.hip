@@ -77,7 +77,7 @@ struct Best {
       mine += k > list;
       place += k > keys;
     }
-    if (least || lane64(list, 0)) {
+    if (lane64(list, 0)) {
       for (int j = 0; j < n; ++j) place += lane64(list, j) > keys;
     }
     // no list has a 64th entry: what has no place goes there
@@ -152,15 +152,19 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
       }
     }
 
-    float most, s;
+    float most, s, high[4];  // of eight each
     auto weigh = [&](auto rare) {
-      most = y[0];
 #pragma unroll
-      for (int i = 1; i < 32; ++i) most = fmaxf(most, y[i]);
-      float top = most;
+      for (int j = 0; j < 4; ++j) {
+        high[j] = y[8 * j];
 #pragma unroll
-      for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-      if (top > ref + kSlackLogit) {
+        for (int i = 1; i < 8; ++i) high[j] = fmaxf(high[j], y[8 * j + i]);
+      }
+      most = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+      if (__any(most > ref + kSlackLogit)) {
+        float top = most;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
         if (ref > -INFINITY) sum *= exp((double)ref - (double)top);
         ref = top;
         less = ref * kLog2eHi;
@@ -219,10 +223,10 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
     }
     // few, or many equal ones: one after the other
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      if (!(__ballot(y[j] >= bound) | __ballot(y[j + 1] >= bound) | __ballot(y[j + 2] >= bound) | __ballot(y[j + 3] >= bound))) continue;
+    for (int j = 0; j < 4; ++j) {
+      if (!__any(high[j] >= bound)) continue;
 #pragma unroll
-      for (int i = j; i < j + 4; ++i) {
+      for (int i = 8 * j; i < 8 * j + 8; ++i) {
         uint64_t mask = __ballot(y[i] >= bound);
         while (mask) {
           const int from = __ffsll((long long)mask) - 1;
@@ -247,41 +251,38 @@ __global__ __launch_bounds__(1024) void pick_kernel(const SelectArgs A) {
   constexpr int kMost = LORA_BEAM_MAX;
   __shared__ double s_rank[kMost * kMost], s_total[kMost * kMost];
   __shared__ int32_t s_token[kMost * kMost];
-  __shared__ float s_score[kMost];
   __shared__ int32_t s_length[kMost], s_done[kMost], s_chosen;
-  const int W = A.beams, row0 = blockIdx.x * W;
+  const int W = A.beams, row0 = blockIdx.x * W, keys = A.waves * W;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  if (threadIdx.x < W) {
-    s_score[threadIdx.x] = A.score[row0 + threadIdx.x];
-    s_length[threadIdx.x] = A.length[row0 + threadIdx.x];
-    s_done[threadIdx.x] = A.done[row0 + threadIdx.x];
-  }
   if (threadIdx.x == 0) s_chosen = 0;
-  __syncthreads();
   for (int w = wave; w < W; w += waves) {
-    const float score = s_score[w];
-    const bool live = fabsf(score) < INFINITY, done = s_done[w] != 0;
+    const int64_t at = (int64_t)(row0 + w) * A.waves;
+    // one trip to memory: what a row that is not continued left there is not used
+    const float score = A.score[row0 + w];
+    const int32_t length = A.length[row0 + w];
+    const bool live = fabsf(score) < INFINITY, done = A.done[row0 + w] != 0;
+    uint64_t key = lane < keys ? A.keys[at * W + lane] : 0;
+    double ref = lane < A.waves ? A.sums[2 * (at + lane)] : -INFINITY, sum = lane < A.waves ? A.sums[2 * (at + lane) + 1] : 0.0;
     double total = -INFINITY;
     int token = -1;
     if (live && done) {
       if (lane == 0) total = score, token = A.eos;
     } else if (live) {
-      const int64_t at = (int64_t)(row0 + w) * A.waves;
-      double ref = -INFINITY;
-      for (int i = lane; i < A.waves; i += 64) ref = fmax(ref, A.sums[2 * (at + i)]);
+      const double mine = ref;
+      for (int i = lane + 64; i < A.waves; i += 64) ref = fmax(ref, A.sums[2 * (at + i)]);
 #pragma unroll
       for (int d = 32; d; d >>= 1) ref = fmax(ref, __shfl_xor(ref, d));
-      double sum = 0.0;
-      for (int i = lane; i < A.waves; i += 64) {
+      sum = mine > -INFINITY ? sum * exp(mine - ref) : 0.0;
+      for (int i = lane + 64; i < A.waves; i += 64) {
         const double r = A.sums[2 * (at + i)];
         if (r > -INFINITY) sum += A.sums[2 * (at + i) + 1] * exp(r - ref);
       }
 #pragma unroll
       for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
       Best best;
-      const int keys = A.waves * W;
-      for (int i0 = 0; i0 < keys; i0 += 64) {
-        const uint64_t key = i0 + lane < keys ? A.keys[at * W + i0 + lane] : 0;
+      best.merge(key, min(keys, 64), W);
+      for (int i0 = 64; i0 < keys; i0 += 64) {
+        key = i0 + lane < keys ? A.keys[at * W + i0 + lane] : 0;
         best.merge(key, min(keys - i0, 64), W);
       }
       if (lane < W && best.list) {
@@ -291,9 +292,10 @@ __global__ __launch_bounds__(1024) void pick_kernel(const SelectArgs A) {
     }
     if (lane < W) {
       double rank = total;
-      if (A.penalty != 0.0) rank = total / pow((double)max(s_length[w] + (done ? 0 : 1), 1), A.penalty);
+      if (A.penalty != 0.0) rank = total / pow((double)max(length + (done ? 0 : 1), 1), A.penalty);
       s_rank[w * W + lane] = rank, s_total[w * W + lane] = total, s_token[w * W + lane] = token;
     }
+    if (lane == 0) s_length[w] = length, s_done[w] = done;
   }
   __syncthreads();
   // each candidate's place: a row's lie in their order, so of another row's the

@@ -31,6 +31,7 @@ extern "C" {
 #define LORA_BEAM_MAX 32               /* beams of a request */
 #define LORA_BEAM_MAX_VOCAB (1 << 24)
 #define LORA_BEAM_MAX_LAYERS 1024      /* caches of one lora_beam_copy */
+#define LORA_BEAM_MAX_PENALTY 16       /* powers of length, of either sign */
 
 /* State of the beams, one entry per row. */
 typedef struct {
@@ -51,7 +52,7 @@ typedef struct {
  *   total = score[r] + x[v] - log(sum_u e^x[u]),  length[r] + 1 tokens,
  * and a row that is done offers itself alone: total = score[r], its length,
  * the token eos.  Candidates are ranked by total / max(length, 1)^length_penalty
- * (0: by total; any finite power), the highest first, equal ones by the lower
+ * (0: by total), the highest first, equal ones by the lower
  * row, then the higher logit, then the lower token.  Sums and ranks are formed in 64 bits (exponentials in
  * 32), from logits of 16 or 32; totals are rounded once, to fp32.
  * A logit of -inf is never chosen.  Where a request has fewer candidates than

@@ -24,7 +24,7 @@ def test_library_exports_every_declared_function():
 
 def test_binding_constants_match_header():
     defs = dict(re.findall(r"^#define (LORA_BEAM_[A-Z_0-9]+) \(?([^/\n]*?)\)?\s*(?:/\*.*)?$", open(HEADER).read(), flags=re.M))
-    want = {"MAX": beam.MAX_BEAMS, "MAX_VOCAB": beam.MAX_VOCAB, "MAX_LAYERS": beam.MAX_LAYERS}
+    want = {"MAX": beam.MAX_BEAMS, "MAX_VOCAB": beam.MAX_VOCAB, "MAX_LAYERS": beam.MAX_LAYERS, "MAX_PENALTY": beam.MAX_PENALTY}
     want.update({f"FLAG_{n}": getattr(beam, f"FLAG_{n}") for n in ("LOGITS", "PARENT", "LENGTH", "FREE_LIST", "BLOCK_RANGE")})
     want.update({f"COUNT_{n}": getattr(beam, f"COUNT_{n}") for n in ("COPIES", "FREED", "FLAGS")})
     assert set(want) == {n[len("LORA_BEAM_"):] for n in defs}
@@ -64,7 +64,7 @@ def beams_at(b, k):
 @pytest.mark.parametrize("case,code", [
     ("null_logits", -1), ("null_parent", -1), ("null_token", -1), ("null_in", -1), ("null_out", -1), ("null_score", -1), ("null_done_out", -1),
     ("null_ws", -1), ("requests", -1), ("beams", -1), ("many_beams", -6), ("vocab", -1), ("large_vocab", -6), ("rows", -6), ("stride", -1),
-    ("far", -6), ("penalty", -1), ("penalty_inf", -1), ("eos", -1), ("eos_low", -1), ("dtype", -6), ("align", -7), ("ws_align", -7), ("ws", -4),
+    ("far", -6), ("penalty", -1), ("penalty_inf", -1), ("penalty_large", -1), ("eos", -1), ("eos_low", -1), ("dtype", -6), ("align", -7), ("ws_align", -7), ("ws", -4),
     ("same_out", -1), ("out_in", -1), ("crossed", -1), ("shifted", -1), ("out_logits", -1),
 ])
 def test_select_refusals(case, code):
@@ -109,6 +109,8 @@ def test_select_refusals(case, code):
         pen = math.nan
     if case == "penalty_inf":
         pen = math.inf
+    if case == "penalty_large":
+        pen = -16.5
     if case == "eos":
         eos = 100
     if case == "eos_low":

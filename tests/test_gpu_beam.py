@@ -181,6 +181,15 @@ def test_beams_that_are_done_or_dead():
             assert got[2][c] == np.float32(score[p]) and got[3][c] == length[p]
 
 
+@pytest.mark.parametrize("penalty", [16.0, -16.0])
+def test_steep_powers_of_length_next_to_dead_rows(penalty):
+    x, score, length, done = random_case(8, 4, 3, 60)
+    score[[1, 5]] = -np.inf
+    length = np.array([2 ** 30, 5, 0, 1, 2, 3] * 2)
+    s = Select(x, 3, score, length, done, 7, penalty, "f32")
+    s.check(s.run(), same=False)
+
+
 def test_start_and_in_place_steps():
     B, W, V = 3, 4, 700
     rng = np.random.default_rng(2)
