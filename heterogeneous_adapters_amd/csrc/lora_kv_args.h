@@ -83,6 +83,7 @@ struct SharedArgs : AttendArgs {
   const int32_t* token_seq;
   float* part_ml;
   int32_t groups, row_cap, list;
+  int32_t first_items;  // of list 0 in the launch of list 1
 };
 
 struct PromptArgs {

@@ -100,10 +100,7 @@ LORA_KV_HD inline int last_row(int first, int rows, int len) {
 // partial results that a last launch joins.
 constexpr int kLists = 4;      // a shared plan's lists: 0 the groups' prefixes, 1 + c the requests' rests of class c
 constexpr int kShareItem = 3;  // int4 per item
-// Smallest chunk of a prefix, and the items (over all kv heads) that a plan
-// splits prefixes into.
-constexpr int kMinPrefixChunk = 512;
-constexpr int kTargetPrefix = 256;
+constexpr int kMinPrefixChunk = 512;  // smallest chunk of a prefix
 // counts of a shared plan: kLists item counts, then
 constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShareCheck = 8, kNumShare = 16;
 
@@ -113,10 +110,13 @@ LORA_KV_HD inline int prefix_class(int64_t T, int64_t G, int64_t groups, int hea
   const int64_t rows = T * G;
   return rows <= kUnit * groups ? 0 : rows <= kMidMost * groups ? 1 : rows <= kWideRows * groups || head_dim > 128 ? 2 : 3;
 }
+// Items (over all kv heads) that a plan splits prefixes into: as many
+// work-groups as the chip holds of a class's kernel at once.
+LORA_KV_HD inline int prefix_items(int cls) { return cls <= 1 ? kTargetItems : cls == 2 ? 512 : 256; }
 // Most items of the prefix list: sum of tiles_g ceil(prefix_g / chunk) <=
-// kTargetPrefix / hkv + sum of tiles_g by the choice of the chunk.
+// prefix_items / hkv + sum of tiles_g by the choice of the chunk.
 LORA_KV_HD inline int64_t prefix_cap(int cls, int64_t T, int64_t groups, int64_t hkv, int64_t G) {
-  return kTargetPrefix / hkv + 1 + T * G / rows_of_class(cls) + 1 + groups;
+  return prefix_items(cls) / hkv + 1 + T * G / rows_of_class(cls) + 1 + groups;
 }
 LORA_KV_HD inline int64_t share_item_cap(int64_t T, int64_t B, int64_t groups, int64_t hkv, int64_t G) {
   return item_cap(T, B, hkv, G) + groups;
@@ -124,7 +124,8 @@ LORA_KV_HD inline int64_t share_item_cap(int64_t T, int64_t B, int64_t groups, i
 // Most rows of partial results: a list's rows once, and as many again as the
 // rows of the items that its chunks add.
 LORA_KV_HD inline int64_t share_row_cap(int64_t T, int64_t hkv, int64_t G) {
-  return 2 * T * G + kPrefixRows * (kTargetPrefix / hkv + 1) + kMidRows * (kTargetItems / hkv + 1) +
+  return 2 * T * G + 65536 / hkv + kPrefixRows +  // class 2: 128 x 512, class 3: 256 x 256
+          kMidRows * (kTargetItems / hkv + 1) +
          kWideRows * (kTargetWide / hkv + 1);
 }
 LORA_KV_HD inline int32_t share_word(const int32_t* share) {

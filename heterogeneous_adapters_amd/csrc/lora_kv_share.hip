@@ -31,12 +31,7 @@ __device__ __forceinline__ void each(F f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-// The group of request i, or -1.
-__device__ __forceinline__ int group_of(const ShareArgs& A, int i) {
-  if (A.groups == 0 || A.group_indptr[0] > i) return -1;
-  const int g = bisect(A.group_indptr, A.groups, i);
-  return i < A.group_indptr[g + 1] ? g : -1;
-}
+constexpr int kLdsGroups = 1024;  // groups whose bounds and cuts lie in LDS
 
 __device__ __forceinline__ int load_now(const int32_t* p) {  // what atomics left there
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -44,7 +39,7 @@ __device__ __forceinline__ int load_now(const int32_t* p) {  // what atomics lef
 
 // One entry of a list: rows that attend to the same keys.
 struct Entry {
-  int list, seq, qs, rows, pos0, kv, base, chunk;
+  int list, seq, qs, rows, pos0, kv, base, chunk, group;
 };
 
 // One work-group: integer work on a few kilobytes per step.
@@ -54,8 +49,26 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
   __shared__ int64_t s_read[3][kWavesP];
   __shared__ int32_t s_item[kLists][kThreads], s_list[kThreads], s_seq[kThreads], s_qs[kThreads], s_rows[kThreads],
       s_pos0[kThreads], s_kv[kThreads], s_base[kThreads], s_chunk[kThreads], s_part[kThreads];
+  __shared__ int32_t s_bounds[kLdsGroups + 1], s_cut[kLdsGroups], s_first[kLdsGroups];
   const int tid = threadIdx.x;
   const int32_t* c = A.counts;
+  const bool in_lds = A.groups <= kLdsGroups;
+  const int32_t* bounds = in_lds ? s_bounds : A.group_indptr;
+  int32_t *cut = in_lds ? s_cut : A.cut, *first_of = in_lds ? s_first : A.first;
+  // a request's rows and length: read along with the counters, used after them
+  const int at0 = tid < A.B ? A.q_indptr[tid] : 0, at1 = tid < A.B ? A.q_indptr[tid + 1] : 0, kv0 = tid < A.B ? A.kv_len[tid] : 0;
+  int flags = 0;
+  for (int g = tid; g < A.groups; g += kThreads) {
+    const int a = A.group_indptr[g], b = A.group_indptr[g + 1], n = A.shared_len[g];
+    const bool bad = a < 0 || b < a || b > A.B || n < 0;
+    if (bad) flags |= LORA_KV_FLAG_GROUPS;
+    cut[g] = bad ? 0 : n;
+    first_of[g] = 0x7fffffff;
+    if (in_lds) {
+      s_bounds[g] = a;
+      if (g == A.groups - 1) s_bounds[g + 1] = b;
+    }
+  }
   const bool built = c[kCountCheck] == check_word(c[kCountB], c[kCountT], c[kCountItems], c[kCountMid], c[kCountWide], c[kCountParts]) &&
                      c[kCountB] == A.B && c[kCountT] == A.T;
   if (!built) {  // no lists, and a check word that no call accepts
@@ -64,48 +77,52 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
     return;
   }
   const bool many = many_rows(A.T, A.B);
-
-  int flags = 0;
-  for (int g = tid; g < A.groups; g += kThreads) {
-    const int a = A.group_indptr[g], b = A.group_indptr[g + 1], n = A.shared_len[g];
-    const bool bad = a < 0 || b < a || b > A.B || n < 0;
-    if (bad) flags |= LORA_KV_FLAG_GROUPS;
-    A.cut[g] = bad ? 0 : n;
-    A.first[g] = 0x7fffffff;
-  }
   __syncthreads();
+
+  // The group of request i, or -1.
+  auto group_of = [&](int i) {
+    if (A.groups == 0 || bounds[0] > i) return -1;
+    const int g = bisect(bounds, A.groups, i);
+    return i < bounds[g + 1] ? g : -1;
+  };
   // what every row of the group sees, and the first request with rows
+  int group0 = -1, pos0 = 0;  // of request tid
   for (int i = tid; i < A.B; i += kThreads) {
-    const int at = A.q_indptr[i], g = A.q_indptr[i + 1] > at ? group_of(A, i) : -1;
+    const bool mine = i == tid;
+    const int at = mine ? at0 : A.q_indptr[i], end = mine ? at1 : A.q_indptr[i + 1];
+    const int pos = end > at ? A.positions[at] : 0, g = end > at ? group_of(i) : -1;
+    if (mine) group0 = g, pos0 = pos;
     if (g < 0) continue;
-    atomicMin(&A.cut[g], min(A.positions[at], A.kv_len[i]));
-    atomicMin(&A.first[g], i);
+    atomicMin(&cut[g], min(pos, mine ? kv0 : A.kv_len[i]));
+    atomicMin(&first_of[g], i);
   }
   __syncthreads();
 
   auto prefix_of = [&](int g) {  // tokens that the group's rows attend to together
-    return g < 0 || load_now(&A.first[g]) == 0x7fffffff ? 0 : load_now(&A.cut[g]) & ~(kUnit - 1);
+    return g < 0 || load_now(&first_of[g]) == 0x7fffffff ? 0 : load_now(&cut[g]) & ~(kUnit - 1);
   };
   auto group_entry = [&](int g) {
-    Entry e{0, 0, 0, 0, 1 << 30, 0, 0, 0};
+    Entry e{0, 0, 0, 0, 1 << 30, 0, 0, 0, -1};
     if (g >= A.groups) return e;
     e.kv = prefix_of(g);
     if (e.kv == 0) return e;
-    e.seq = load_now(&A.first[g]);
-    e.qs = A.q_indptr[A.group_indptr[g]];
-    e.rows = (A.q_indptr[A.group_indptr[g + 1]] - e.qs) * A.G;
+    e.seq = load_now(&first_of[g]);
+    e.qs = A.q_indptr[bounds[g]];
+    e.rows = (A.q_indptr[bounds[g + 1]] - e.qs) * A.G;
     return e;
   };
   auto request_entry = [&](int i) {
-    Entry e{1, i, 0, 0, 0, 0, 0, 0};
+    Entry e{1, i, 0, 0, 0, 0, 0, 0, -1};
     if (i >= A.B) return e;
-    e.qs = A.q_indptr[i];
-    e.rows = (A.q_indptr[i + 1] - e.qs) * A.G;
+    const bool mine = i == tid;
+    e.qs = mine ? at0 : A.q_indptr[i];
+    e.rows = ((mine ? at1 : A.q_indptr[i + 1]) - e.qs) * A.G;
     if (e.rows == 0) return e;
     e.list = 1 + (e.rows <= kUnit || !many ? 0 : e.rows <= kMidMost ? 1 : 2);
-    e.base = prefix_of(group_of(A, i));
-    e.pos0 = A.positions[e.qs] - e.base;
-    e.kv = A.kv_len[i] - e.base;
+    e.group = mine ? group0 : group_of(i);
+    e.base = prefix_of(e.group);
+    e.pos0 = (mine ? pos0 : A.positions[e.qs]) - e.base;
+    e.kv = (mine ? kv0 : A.kv_len[i]) - e.base;
     return e;
   };
   auto class_of_list = [&](int list) { return list == 0 ? A.prefix_class : list - 1; };
@@ -113,15 +130,16 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
     const int per = rows_of_class(class_of_list(e.list));
     return (e.rows + per - 1) / per;
   };
+  const Entry mine_g = group_entry(tid), mine_r = request_entry(tid);
 
   // Tokens per item, from the keys that all tiles read.
   int64_t reads[3] = {0, 0, 0};
   for (int g = tid; g < A.groups; g += kThreads) {
-    const Entry e = group_entry(g);
+    const Entry e = g == tid ? mine_g : group_entry(g);
     reads[0] += (int64_t)tiles_of(e) * e.kv;
   }
   for (int i = tid; i < A.B; i += kThreads) {
-    const Entry e = request_entry(i);
+    const Entry e = i == tid ? mine_r : request_entry(i);
     reads[e.list == 3 ? 2 : 1] += (int64_t)tiles_of(e) * e.kv;
   }
 #pragma unroll
@@ -137,14 +155,14 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
     const int64_t per = (sum * A.hkv + target - 1) / target;
     return (int)min(max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)least), (int64_t)1 << 29);
   };
-  const int chunk0 = chunk_for(s_read[0], kTargetPrefix, kMinPrefixChunk), chunk1 = chunk_for(s_read[1], kTargetItems, kMinChunk),
+  const int chunk0 = chunk_for(s_read[0], prefix_items(A.prefix_class), kMinPrefixChunk), chunk1 = chunk_for(s_read[1], kTargetItems, kMinChunk),
             chunk2 = chunk_for(s_read[2], kTargetWide, kMinChunk);
 
   int64_t items0[kLists] = {0, 0, 0, 0}, rows0 = 0;
   // Lists the entries of one kind and says where their partial results are.
-  auto emit = [&](int count, auto entry, auto note) {
+  auto emit = [&](int count, const Entry& mine, auto entry, auto note) {
     for (int first = 0; first < count; first += kThreads) {
-      Entry e = entry(first + tid);
+      Entry e = first == 0 ? mine : entry(first + tid);
       if (first + tid >= count) e.rows = 0;
       const int tiles = tiles_of(e);
       e.chunk = even_chunk(e.kv, e.list == 0 ? chunk0 : e.list == 3 ? chunk2 : chunk1);
@@ -182,13 +200,13 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
   };
   // A prefix's partial results: of its first row's first chunk, chunks, first
   // token row, rows.
-  emit(A.groups, group_entry, [&](int g, const Entry& e, int part, int chunks) {
+  emit(A.groups, mine_g, group_entry, [&](int g, const Entry& e, int part, int chunks) {
     if (g < A.groups) A.group_parts[g] = make_int4(part, chunks, e.qs, e.rows);
   });
   __syncthreads();
-  emit(A.B, request_entry, [&](int i, const Entry& e, int part, int chunks) {
+  emit(A.B, mine_r, request_entry, [&](int i, const Entry& e, int part, int chunks) {
     if (i >= A.B) return;
-    const int g = e.base > 0 ? group_of(A, i) : -1;
+    const int g = e.base > 0 ? e.group : -1;
     A.seq_parts[2 * i] = g < 0 ? make_int4(0, 0, 0, 0) : A.group_parts[g];
     A.seq_parts[2 * i + 1] = make_int4(part, chunks, e.qs, e.rows);
   });
@@ -542,8 +560,11 @@ hipError_t launch(SharedArgs A, int prefix_cls, bool many, hipStream_t s) {
       else attend_kernel<E, NC, 2, 3, SharedArgs><<<n * (kPrefixRows / kMidRows), 64 * kWaves, 0, s>>>(A);
     }
   };
-  if (A.groups > 0) run(0, prefix_cls, prefix_cap(prefix_cls, A.T, A.groups, hkv, A.G));
-  for (int c = many ? 2 : 0; c >= 0; --c) run(1 + c, c, class_cap(c, A.T, A.B, hkv, A.G));
+  A.first_items = 0;
+  if (A.groups > 0 && prefix_cls == 0) A.first_items = (int32_t)prefix_cap(0, A.T, A.groups, hkv, A.G);
+  else if (A.groups > 0) run(0, prefix_cls, prefix_cap(prefix_cls, A.T, A.groups, hkv, A.G));
+  for (int c = many ? 2 : 1; c > 0 && many; --c) run(1 + c, c, class_cap(c, A.T, A.B, hkv, A.G));
+  run(1, 0, A.first_items + class_cap(0, A.T, A.B, hkv, A.G));
   const int vecs = 8 * NC;
   const int64_t tasks = (int64_t)A.T * hkv * A.G * vecs;
   join_kernel<E><<<(unsigned)((tasks + 255) / 256), 256, 0, s>>>(A, vecs);

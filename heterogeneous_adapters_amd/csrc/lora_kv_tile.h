@@ -120,13 +120,16 @@ __device__ __forceinline__ bool read_item(const AttendArgs& A, int cls, int coun
 // An item of a shared step (lora_kv_share): keys of a group's prefix or of a
 // request's rest, always to a partial result.
 __device__ __forceinline__ bool read_item(const SharedArgs& A, int, int, int item, int skip, int rows, Item& it) {
-  const int4* d = A.items + kShareItem * ((int64_t)A.list * A.item_cap + item);
+  // list 1's launch takes list 0's items of 16 rows along, before its own
+  const int list = A.list == 1 && item < A.first_items ? 0 : A.list;
+  if (A.list == 1 && list == 1) item -= A.first_items;
+  const int4* d = A.items + kShareItem * ((int64_t)list * A.item_cap + item);
   const int4 x = d[0], y = d[1], z = d[2];
   if (!share_ok(A)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
     return false;
   }
-  if (item >= A.share[A.list]) return false;
+  if (item >= A.share[list]) return false;
   it.seq = uniform(x.x), it.row0 = uniform(x.y) + skip, it.part = uniform(x.z), it.base = uniform(x.w);
   it.qs = uniform(y.x), it.nrows = uniform(y.y), it.pos0 = uniform(y.z), it.kv = uniform(y.w);
   if (it.row0 >= it.nrows) return false;
