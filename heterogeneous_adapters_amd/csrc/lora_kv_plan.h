@@ -100,19 +100,25 @@ LORA_KV_HD inline int last_row(int first, int rows, int len) {
 // partial results that a last launch joins.
 constexpr int kLists = 4;      // a shared plan's lists: 0 the groups' prefixes, 1 + c the requests' rests of class c
 constexpr int kShareItem = 3;  // int4 per item
-constexpr int kMinPrefixChunk = 512;  // smallest chunk of a prefix
+LORA_KV_HD inline int min_prefix_chunk(int cls) { return cls == 0 ? 512 : 256; }  // smallest chunk of a prefix
 // counts of a shared plan: kLists item counts, then
 constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShareCheck = 8, kNumShare = 16;
 
 // Rows of a prefix's item, as a class, by the groups' average (the host's
-// arithmetic; sizes of single groups are known to the device only).
+// arithmetic; sizes of single groups and prefixes are known to the device
+// only). Few rows: items of 16, which go with the requests' rests in one launch
+// and read the prefix again from the caches for every 16 rows. More: class 3, or
+// 2 where 256 rows' registers do not suffice. Prefixes of 4000 and 16384, 32 heads on
+// 8 of 128, in 16-row items and else: 240 rows 19 (2000) and 44 us, 34 (2000)
+// and 45; 320 rows 29 and 62, 38 and 57; 512 rows 34 and 74, 41 and 62; 1024 rows
+// 51 and 128, 52 and 94. 200 rows of 256 dims: 63 and 54 us.
+constexpr int kFewRows = 320, kFewRowsFar = 128;  // up to 128 dims, and past them
 LORA_KV_HD inline int prefix_class(int64_t T, int64_t G, int64_t groups, int head_dim) {
-  const int64_t rows = T * G;
-  return rows <= kUnit * groups ? 0 : rows <= kMidMost * groups ? 1 : rows <= kWideRows * groups || head_dim > 128 ? 2 : 3;
+  return T * G <= (head_dim > 128 ? kFewRowsFar : kFewRows) * groups ? 0 : head_dim > 128 ? 2 : 3;
 }
 // Items (over all kv heads) that a plan splits prefixes into: as many
 // work-groups as the chip holds of a class's kernel at once.
-LORA_KV_HD inline int prefix_items(int cls) { return cls <= 1 ? kTargetItems : cls == 2 ? 512 : 256; }
+LORA_KV_HD inline int prefix_items(int cls) { return cls == 0 ? kTargetItems : cls == 2 ? 512 : 256; }
 // Most items of the prefix list: sum of tiles_g ceil(prefix_g / chunk) <=
 // prefix_items / hkv + sum of tiles_g by the choice of the chunk.
 LORA_KV_HD inline int64_t prefix_cap(int cls, int64_t T, int64_t groups, int64_t hkv, int64_t G) {
@@ -124,8 +130,8 @@ LORA_KV_HD inline int64_t share_item_cap(int64_t T, int64_t B, int64_t groups, i
 // Most rows of partial results: a list's rows once, and as many again as the
 // rows of the items that its chunks add.
 LORA_KV_HD inline int64_t share_row_cap(int64_t T, int64_t hkv, int64_t G) {
-  return 2 * T * G + 65536 / hkv + kPrefixRows +  // class 2: 128 x 512, class 3: 256 x 256
-          kMidRows * (kTargetItems / hkv + 1) +
+  return 2 * T * G + 65536 / hkv + kPrefixRows +  // prefixes of class 2: 128 x 512, of class 3: 256 x 256
+         kMidRows * (kTargetItems / hkv + 1) +
          kWideRows * (kTargetWide / hkv + 1);
 }
 LORA_KV_HD inline int32_t share_word(const int32_t* share) {

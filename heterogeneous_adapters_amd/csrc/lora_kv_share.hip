@@ -31,6 +31,7 @@ __device__ __forceinline__ void each(F f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
+constexpr int kFewTasks = 1 << 16;   // joins of up to as many vectors
 constexpr int kLdsGroups = 1024;  // groups whose bounds and cuts lie in LDS
 
 __device__ __forceinline__ int load_now(const int32_t* p) {  // what atomics left there
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
     const int64_t per = (sum * A.hkv + target - 1) / target;
     return (int)min(max((per + kChunkStep - 1) / kChunkStep * kChunkStep, (int64_t)least), (int64_t)1 << 29);
   };
-  const int chunk0 = chunk_for(s_read[0], prefix_items(A.prefix_class), kMinPrefixChunk), chunk1 = chunk_for(s_read[1], kTargetItems, kMinChunk),
+  const int chunk0 = chunk_for(s_read[0], prefix_items(A.prefix_class), min_prefix_chunk(A.prefix_class)), chunk1 = chunk_for(s_read[1], kTargetItems, kMinChunk),
             chunk2 = chunk_for(s_read[2], kTargetWide, kMinChunk);
 
   int64_t items0[kLists] = {0, 0, 0, 0}, rows0 = 0;
@@ -493,40 +494,69 @@ __global__ __launch_bounds__(512, 2) void prefix_kernel(const SharedArgs A) {
   }
 }
 
-// Four dims of a row per thread.
-template <class E>
+// Four dims of a row by kGroups threads of a work-group, each every kGroups-th
+// result, joined in a fixed order.
+template <class E, int kGroups>
 __global__ __launch_bounds__(256) void join_kernel(const SharedArgs A, int vecs) {
   typedef typename E::T T;
+  constexpr int kBatch = 4, kTasks = 256 / kGroups;  // results in flight; tasks of a work-group
+  __shared__ float s_part[kGroups > 1 ? 256 : 1][6];
   if (!share_ok(A)) return;  // the lists' launches have flagged it
   const int D = vecs * 4, hkv = A.cache.heads, hq = hkv * A.G;
-  const int64_t task = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int grp = threadIdx.x / kTasks;
+  const int64_t task = (int64_t)blockIdx.x * kTasks + threadIdx.x % kTasks;
   const int d = (int)(task % vecs) * 4, h = (int)(task / vecs % hq);
   const int64_t t = task / vecs / hq;
-  if (t >= A.T) return;
-  const int seq = A.token_seq[t];
-  if ((unsigned)seq >= (unsigned)A.B) return;
+  const int seq = t < A.T ? A.token_seq[t] : -1;
+  const bool live = (unsigned)seq < (unsigned)A.B;
   const int kvh = h / A.G, hg = h - kvh * A.G;
   float M = kNone, L = 0.0f;
   f4 acc{0, 0, 0, 0};
+  auto add = [&](float m, float l, f4 o) {
+    const float mn = fmaxf(M, m), a = exp2_hw(M - mn), b = exp2_hw(m - mn);
+    M = mn;
+    L = L * a + l * b;
+    acc = acc * a + b * o;
+  };
+  if (live) {
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const int4 p = A.seq_parts[2 * seq + side];  // first result's row, chunks, first token row, rows
-    const int row = ((int)t - p.z) * A.G + hg;
-    // a batch built again after its shared plan
-    if (p.y > 0 && ((int)t < p.z || row >= p.w)) {
-      if (d == 0 && hg == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
-      continue;
-    }
-    for (int c = 0; c < p.y; ++c) {
-      const int64_t at = (int64_t)(p.x + c * p.w + row) * hkv + kvh;
-      const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
-      const f4 o = *reinterpret_cast<const f4*>(A.part + at * D + d);
-      const float mn = fmaxf(M, ml.x), a = exp2_hw(M - mn), b = exp2_hw(ml.x - mn);
-      M = mn;
-      L = L * a + ml.y * b;
-      acc = acc * a + b * o;
+    for (int side = 0; side < 2; ++side) {
+      const int4 p = A.seq_parts[2 * seq + side];  // first result's row, chunks, first token row, rows
+      const int row = ((int)t - p.z) * A.G + hg;
+      // a batch built again after its shared plan
+      if (p.y > 0 && ((int)t < p.z || row >= p.w)) {
+        if (d == 0 && hg == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
+        continue;
+      }
+      for (int c0 = grp; c0 < p.y; c0 += kBatch * kGroups) {
+        float2 ml[kBatch];
+        f4 o[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int64_t at = (int64_t)(p.x + min(c0 + e * kGroups, p.y - 1) * p.w + row) * hkv + kvh;
+          ml[e] = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
+          o[e] = *reinterpret_cast<const f4*>(A.part + at * D + d);
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          if (c0 + e * kGroups >= p.y) break;
+          add(ml[e].x, ml[e].y, o[e]);
+        }
+      }
     }
   }
+  if constexpr (kGroups > 1) {
+    float* s = s_part[threadIdx.x];
+    s[0] = M, s[1] = L, s[2] = acc[0], s[3] = acc[1], s[4] = acc[2], s[5] = acc[3];
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int e = 1; e < kGroups; ++e) {
+      const float* o = s_part[threadIdx.x + e * kTasks];
+      add(o[0], o[1], f4{o[2], o[3], o[4], o[5]});
+    }
+  }
+  if (!live) return;
   const float inv = inverse(L);
   T* out = static_cast<T*>(A.o.p) + t * A.o.ts + h * A.o.hs + d;
   if constexpr (sizeof(T) == 2) {
@@ -539,35 +569,38 @@ __global__ __launch_bounds__(256) void join_kernel(const SharedArgs A, int vecs)
 template <class E, int NC>
 hipError_t launch(SharedArgs A, int prefix_cls, bool many, hipStream_t s) {
   const int hkv = A.cache.heads;
-  auto run = [&](int list, int cls, int64_t items) {
+  auto blocks = [&](int list, int64_t items) {
     A.list = list;
-    const unsigned n = (unsigned)(items * hkv);
-    if constexpr (sizeof(typename E::T) == 2) {
-      if constexpr (NC <= 4) {
-        if (list == 0 && cls == 3) {
-          prefix_kernel<NC><<<n, 512, 0, s>>>(A);
-          return;
-        }
-      }
-    }
-    if (cls == 0) {
-      attend_kernel<E, NC, 1, 0, SharedArgs><<<n, 64 * kWaves, 0, s>>>(A);
-    } else if (cls == 1) {
-      attend_kernel<E, NC, 2, 1, SharedArgs><<<n, 64 * kWaves, 0, s>>>(A);
-    } else {
-      if constexpr (sizeof(typename E::T) == 2) attend_wide_kernel<NC, SharedArgs><<<n, 256, 0, s>>>(A);
-      else if (cls == 2) attend_kernel<E, NC, 2, 2, SharedArgs><<<n * (kWideRows / kMidRows), 64 * kWaves, 0, s>>>(A);
-      else attend_kernel<E, NC, 2, 3, SharedArgs><<<n * (kPrefixRows / kMidRows), 64 * kWaves, 0, s>>>(A);
-    }
+    return (unsigned)(items * hkv);
   };
+  constexpr bool kBf16 = sizeof(typename E::T) == 2;
   A.first_items = 0;
-  if (A.groups > 0 && prefix_cls == 0) A.first_items = (int32_t)prefix_cap(0, A.T, A.groups, hkv, A.G);
-  else if (A.groups > 0) run(0, prefix_cls, prefix_cap(prefix_cls, A.T, A.groups, hkv, A.G));
-  for (int c = many ? 2 : 1; c > 0 && many; --c) run(1 + c, c, class_cap(c, A.T, A.B, hkv, A.G));
-  run(1, 0, A.first_items + class_cap(0, A.T, A.B, hkv, A.G));
+  if (A.groups > 0) {
+    const int64_t items = prefix_cap(prefix_cls, A.T, A.groups, hkv, A.G);
+    if (prefix_cls == 0) {
+      A.first_items = (int32_t)items;
+    } else if (prefix_cls == 2) {
+      const unsigned n = blocks(0, items);
+      if constexpr (kBf16 && NC > 4) attend_wide_kernel<NC, SharedArgs><<<n, 256, 0, s>>>(A);
+      if constexpr (!kBf16 && NC > 4) attend_kernel<E, NC, 2, 2, SharedArgs><<<n * (kWideRows / kMidRows), 64 * kWaves, 0, s>>>(A);
+    } else {
+      const unsigned n = blocks(0, items);
+      if constexpr (kBf16 && NC <= 4) prefix_kernel<NC><<<n, 512, 0, s>>>(A);
+      if constexpr (!kBf16 && NC <= 4) attend_kernel<E, NC, 2, 3, SharedArgs><<<n * (kPrefixRows / kMidRows), 64 * kWaves, 0, s>>>(A);
+    }
+  }
+  if (many) {
+    const unsigned wide = blocks(3, class_cap(2, A.T, A.B, hkv, A.G));
+    if constexpr (kBf16) attend_wide_kernel<NC, SharedArgs><<<wide, 256, 0, s>>>(A);
+    else attend_kernel<E, NC, 2, 2, SharedArgs><<<wide * (kWideRows / kMidRows), 64 * kWaves, 0, s>>>(A);
+    attend_kernel<E, NC, 2, 1, SharedArgs><<<blocks(2, class_cap(1, A.T, A.B, hkv, A.G)), 64 * kWaves, 0, s>>>(A);
+  }
+  attend_kernel<E, NC, 1, 0, SharedArgs><<<blocks(1, A.first_items + class_cap(0, A.T, A.B, hkv, A.G)), 64 * kWaves, 0, s>>>(A);
   const int vecs = 8 * NC;
   const int64_t tasks = (int64_t)A.T * hkv * A.G * vecs;
-  join_kernel<E><<<(unsigned)((tasks + 255) / 256), 256, 0, s>>>(A, vecs);
+  // few rows have many results each: eight threads for one
+  if (tasks <= kFewTasks) join_kernel<E, 8><<<(unsigned)((tasks + 31) / 32), 256, 0, s>>>(A, vecs);
+  else join_kernel<E, 1><<<(unsigned)((tasks + 255) / 256), 256, 0, s>>>(A, vecs);
   return hipGetLastError();
 }
 

@@ -109,6 +109,59 @@ def test_prefixes_in_several_chunks_and_tiles(hq, hkv, D, dtype):
     s.check(s.run(scale), scale)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,P,bt", [(32, 70, 16), (64, 700, 32), (96, 320, 16), (128, 64, 16), (128, 615, 64), (160, 130, 16), (192, 304, 32),
+                                    (224, 77, 16), (256, 560, 16)])
+def test_groups_of_many_rows(D, P, bt, dtype):
+    """32 query heads on one: 352 and 448 rows of a group up to 128 dims, 160 and 288 past them, in tiles of 256 and 128."""
+    n = (11, 14) if D <= 128 else (5, 9)
+    ctx = [P + 3 * i for i in range(n[0])] + [40 + P - i % 2 for i in range(n[1])] + [9]
+    s = SharedStep(D + P, ctx, [1] * len(ctx), [0, n[0], sum(n)], [P, P + 39], 32, 1, D, bt, dtype, by_id=P % 2 == 0, pad=2)
+    scale = 1.0 / math.sqrt(D)
+    s.check(s.run(scale), scale)
+    assert int(s.batch.flags) == 0 and s.counts_of_prefixes() > 0
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("power,D", [(20, 64), (100, 128), (60, 160)])
+def test_scores_far_from_zero_in_tiles_of_many_rows(power, D, order):
+    """Scores of up to 2^power, growing or falling along the keys: all weight on one key."""
+    n, P = (11, 130) if D <= 128 else (5, 130)
+    s = SharedStep(power, [P] * n, [1] * n, [0, n], [P], 32, 1, D, 16, "bf16")
+    at = np.concatenate([[0], np.cumsum([P + 1] * n)])
+    place = np.argsort(np.arange(P))[::order]
+    for i in range(n):
+        s.k[at[i]:at[i + 1]] = 0.0
+        s.k[at[i]:at[i] + P, :, 0] = 2.0 ** (power // 2) * (1 + (place % 4) / 2)[:, None] * np.where(place >= P - 4, 1, 2.0 ** -20)[:, None]
+        pos = np.arange(P + 1)
+        slots = s.ref["table"][i, pos // 16] * 16 + pos % 16
+        R.put(s.data, slots, s.k[at[i]:at[i + 1]], s.v[at[i]:at[i + 1]], 16)
+        s.k[at[i]:at[i + 1]], s.v[at[i]:at[i + 1]] = R.get(s.data, slots, 1, D, 16)  # as 4 bits hold them
+    s.q[:] = 0.0
+    s.q[..., 0] = 2.0 ** (power - power // 2)
+    got = s.run(1.0)
+    for i in range(n):
+        score = s.k[at[i]:at[i + 1], 0, 0] * s.q[i, 0, 0]
+        best = np.flatnonzero(score == score.max())
+        want = R.bf16(s.v[at[i] + best].mean(0))  # the others' weights are 0, these are equal
+        assert np.all(np.abs(got[i] - want) <= 2.0 ** -8 * np.abs(s.v[at[i] + best]).mean(0) + 2.0 ** -8 * np.abs(want))
+
+
+def test_bad_blocks_and_ends_in_tiles_of_many_rows():
+    """A block outside the cache in the middle, bytes of NaN scales behind the last token, two chunks."""
+    n, P = 11, 592
+    s = SharedStep(7, [P] * n, [1] * n, [0, n], [P], 32, 1, 128, 16, "bf16")
+    s.run(0.1)
+    s.tab[0, 5] = -9
+    s.again(0.1)
+    assert int(s.batch.flags) == kv.FLAG_BLOCK_RANGE
+    got, at = host(s.out), np.concatenate([[0], np.cumsum([P + 1] * n)])
+    for i in range(n):
+        keep = np.r_[at[i]:at[i] + 80, at[i] + 96:at[i + 1]]
+        o, a, sa = R.attend_rows(s.q[i:i + 1], s.k[keep], s.v[keep], [len(keep)], 0.1)
+        assert np.all(np.abs(got[i] - o[0]) <= R.attend_bound(o, a, sa, len(keep), 128, "bf16")[0])
+
+
 def test_strided_queries_and_outputs():
     s = SharedStep(2, [100, 130, 140], [1, 5, 1], [0, 3], [96], 4, 2, 64, 16, "bf16")
     s.run(0.125)
