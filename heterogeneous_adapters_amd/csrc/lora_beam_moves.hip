@@ -41,14 +41,16 @@ __device__ __forceinline__ int block_sum(int x, int& before, int* scratch) {
   return all;
 }
 
-// EMIT: the second launch, which writes; the first counts.
-template <bool EMIT>
+// EMIT: the second launch, which writes; the first counts, where there are
+// several requests.  ROWS: at least as many as a request has beams.
+template <bool EMIT, int ROWS>
 __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) {
   __shared__ int s_parent[kMost], s_blocks[kMost], s_len[kMost], s_copy[kMost];  // by new row: parent (-1), blocks, copy's place or -1
   __shared__ int s_old[kMost];                                                   // blocks of the old rows
-  __shared__ int s_sum[kThreads / 64], s_sum2[kThreads / 64], s_copies;
+  __shared__ int s_sum[kThreads / 64], s_sum2[kThreads / 64], s_copies, s_flags;
   const int W = A.beams, b = blockIdx.x, row0 = b * W, tid = threadIdx.x, bt = 1 << A.bt_log2;
   int flags = 0;
+  if (tid == 0) s_flags = 0;
   if (tid < W) {
     const int64_t cap = (int64_t)A.width << A.bt_log2;
     int p = A.parent[row0 + tid], len = A.kv_len[row0 + tid];
@@ -93,13 +95,13 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
   int freed = 0;
   for (int j0 = 0; j0 < A.width; j0 += kThreads) {
     const int j = j0 + tid;
-    int32_t id[kMost];
+    int32_t id[ROWS];
     uint32_t gone = 0;  // rows whose block here nobody holds, the first of those that share it
     if (j < A.width) {
 #pragma unroll
-      for (int r = 0; r < kMost; ++r) id[r] = r < W && j < s_old[r] ? table[r * A.stride + j] : -1;
+      for (int r = 0; r < ROWS; ++r) id[r] = r < W && j < s_old[r] ? table[r * A.stride + j] : -1;
 #pragma unroll
-      for (int r = 0; r < kMost; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         if (r >= W || j >= s_old[r]) continue;
         if ((unsigned)id[r] >= (unsigned)A.num_blocks) {
           if (id[r] != -1) flags |= LORA_BEAM_FLAG_BLOCK_RANGE;
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
         }
         bool out = true;
 #pragma unroll
-        for (int o = 0; o < kMost; ++o) out = out && !(id[o] == id[r] && (o < r || (parents >> o & 1)));
+        for (int o = 0; o < ROWS; ++o) out = out && !(id[o] == id[r] && (o < r || (parents >> o & 1)));
         gone |= out ? 1u << r : 0;
       }
     }
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
     if (EMIT && j < A.width) {
       int to = freed0 + freed + before;
 #pragma unroll
-      for (int r = 0; r < kMost; ++r)
+      for (int r = 0; r < ROWS; ++r)
         if (gone >> r & 1) A.freed[to++] = id[r];
     }
     freed += all;
@@ -151,7 +153,20 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
     for (int i = copies + tid; i < A.max_rows; i += kThreads) A.source[i] = A.target[i] = A.tokens[i] = -1;
     if (tid == 0) A.counts[LORA_BEAM_COUNT_COPIES] = copies, A.counts[LORA_BEAM_COUNT_FREED] = freed0 + freed;
   }
-  if (flags) atomicOr(&A.counts[LORA_BEAM_COUNT_FLAGS], flags);
+  if (A.requests > 1) {
+    if (flags) atomicOr(&A.counts[LORA_BEAM_COUNT_FLAGS], flags);
+    return;
+  }
+  if (flags) atomicOr(&s_flags, flags);  // no launch before this one has cleared them
+  __syncthreads();
+  if (tid == 0) A.counts[LORA_BEAM_COUNT_FLAGS] = s_flags;
+}
+
+// No requests: empty lists.
+__global__ __launch_bounds__(kThreads) void no_moves_kernel(const ReorderArgs A) {
+  for (int i = threadIdx.x; i < A.max_rows; i += kThreads) A.source[i] = A.target[i] = A.tokens[i] = -1;
+  if (threadIdx.x == 0)
+    A.counts[LORA_BEAM_COUNT_COPIES] = A.counts[LORA_BEAM_COUNT_FREED] = A.counts[LORA_BEAM_COUNT_FLAGS] = 0;
 }
 
 // A wave per (copy, layer, kv head): the head's records of a block lie together.
@@ -179,12 +194,24 @@ __global__ __launch_bounds__(256) void copy_kernel(const CopyArgs A) {
   }
 }
 
+template <int ROWS>
+hipError_t reorder(const ReorderArgs& A, hipStream_t s) {
+  if (A.requests > 1) reorder_kernel<false, ROWS><<<A.requests, kThreads, 0, s>>>(A);
+  reorder_kernel<true, ROWS><<<A.requests, kThreads, 0, s>>>(A);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_reorder(const ReorderArgs& A, hipStream_t s) {
-  reorder_kernel<false><<<A.requests, kThreads, 0, s>>>(A);
-  reorder_kernel<true><<<A.requests, kThreads, 0, s>>>(A);
-  return hipGetLastError();
+  if (A.requests == 0) {
+    no_moves_kernel<<<1, kThreads, 0, s>>>(A);
+    return hipGetLastError();
+  }
+  if (A.beams <= 4) return reorder<4>(A, s);
+  if (A.beams <= 8) return reorder<8>(A, s);
+  if (A.beams <= 16) return reorder<16>(A, s);
+  return reorder<32>(A, s);
 }
 
 hipError_t launch_copy(const CopyArgs& A, hipStream_t s) {

@@ -326,6 +326,19 @@ def test_reorder_flags(case):
     assert r.check()["flags"] == {"parent": 2, "length": 4, "free": 8, "free_id": 16, "table_id": 16, "no_free": 8}[case]
 
 
+def test_reorder_of_nothing_empties_the_lists():
+    rng = np.random.default_rng(5)
+    table, free, num = descent(rng, 1, 4, [40], [0], 16)
+    r = Reorder(np.zeros(4, int), 4, np.full(4, 40), table, free, num, 16)
+    r.run()
+    assert int(r.moves.copies) == 3 and int(r.moves.given_back) > 0
+    none = i32([])
+    wide = torch.zeros((0, table.shape[1]), dtype=torch.int32, device=DEV)
+    beam.lora_beam_reorder(none, 4, none, wide, none.clone(), wide.clone(), r.free, num, 16, r.moves)
+    torch.cuda.synchronize()
+    assert (int(r.moves.copies), int(r.moves.given_back), int(r.moves.flags)) == (0, 0, 0) and torch.all(r.moves.source == -1)
+
+
 @pytest.mark.parametrize("layers,hkv,D,bt,extra", [(1, 1, 32, 16, 0), (3, 2, 96, 64, 32), (5, 3, 128, 256, 16), (70, 1, 64, 32, 0), (2, 8, 256, 16, 0)])
 def test_copies_in_every_layer(layers, hkv, D, bt, extra):
     rng = np.random.default_rng(layers)
