@@ -4,8 +4,13 @@
 // kilobytes at most), bound by latency.  A request's beams share blocks at the
 // same column only, so what a column still holds is decided within the
 // request, without reference counts; two launches, because where a request's
-// entries of the lists begin depends on the requests before it.  The copies
-// are bound by HBM.
+// entries of the lists begin depends on the requests before it (one for one
+// request).  The copies are bound by HBM.
+//
+// Measured on MI355X: one request of 4 beams 5.9 us, and 3.8 for the copies in 4
+// layers; 96 requests of 8 beams, up to 2300 tokens in blocks of 64, 5.4 + 10, and
+// 13.6 for 90 MB of copies (read and written). With loops over 32 rows whatever
+// the request's, 10 and 10 + 13 us.
 #include "lora_beam_args.h"
 #include "lora_kv_dev.h"
 

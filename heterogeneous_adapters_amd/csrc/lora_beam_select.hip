@@ -2,13 +2,21 @@
 //
 // Mathematics: a row's candidates are ordered as its logits are, so a row needs
 // its `beams` highest logits and log(sum e^x), both from one pass: a wave
-// holds 2048 logits in registers, sums e^(x - r) against its highest logit r so
-// far (each chunk's sum in fp32 per lane, the chunks' in fp64) and keeps the
-// highest logits so far, one per lane in descending order, as keys (the logit
+// holds 2048 logits in registers, sums e^(x - r) against a logit r that none has
+// passed by more than 8 (each chunk's sum in fp32 per lane, the chunks' in fp64)
+// and keeps the highest logits so far, one per lane in descending order, as keys (the logit
 // as an ordered integer, then the token's complement, so that equal logits go
 // by the lower token).  A chunk whose highest logit is below the last of these
-// is done with its sum.  A second launch joins the waves of each row and ranks the request's
-// beams * beams candidates in 64 bits.
+// is done with its sum.  A second launch joins the waves of each row and ranks
+// the request's beams * beams candidates in 64 bits.
+//
+// Measured on MI355X (rows, then picks): 64 requests of 8 beams, 128000 bf16
+// logits, 32 + 8 us, 4.1 TB/s of logits; without looking for candidates the
+// rows' launch takes 22.5, 5.8 TB/s (the read rate), so what bounds it is the
+// comparisons and insertions of the chunks that follow a wave's first. Fewer,
+// longer waves look less (4096 waves 32 us, 8192 38); waves that tell one another
+// their lowest kept logit gain nothing, as they keep pace. 128 x 16 of 32000 38 + 8 us;
+// 32 x 5 of 50257 fp32 10 + 11; 1 x 4 of 32000 6.8 + 5.4, latency.
 #include <type_traits>
 
 #include "lora_beam_args.h"

@@ -326,6 +326,20 @@ def test_many_requests_and_groups():
     assert int(s.batch.flags) == 0
 
 
+def test_more_groups_than_lds_holds():
+    rng = np.random.default_rng(3)
+    B = 1500
+    groups = np.sort(np.concatenate([[0, B], rng.choice(np.arange(1, B), 1148, replace=False)]))
+    lens = rng.integers(0, 40, len(groups) - 1)
+    assert len(lens) > 1024
+    ctx, new = rng.integers(0, 50, B), np.where(rng.random(B) < 0.1, 0, 1)
+    # a group is read through its first request with tokens
+    first = {g: next((i for i in range(groups[g], groups[g + 1]) if new[i]), int(groups[g])) for g in range(len(lens))}
+    s = SharedStep(12, ctx, new, list(groups), list(lens), 2, 1, 32, 16, "bf16", same=first)
+    s.check(s.run(0.3), 0.3)
+    assert int(s.batch.flags) == 0
+
+
 def test_nothing_to_do():
     b = kv.Batch(4, 4, 4, 2, 64)
     sh = kv.Shared(b, 2)
