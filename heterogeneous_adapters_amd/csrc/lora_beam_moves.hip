@@ -70,17 +70,22 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
     s_blocks[tid] = (n + bt - 1) >> A.bt_log2;
   }
   __syncthreads();
-  if (tid == 0) {
-    int copies = 0;
-    uint32_t kept = 0;  // parents whose open block an earlier row keeps
-    for (int c = 0; c < W; ++c) {
-      const int p = s_parent[c];
-      s_copy[c] = -1;
-      if (p < 0 || (s_len[c] & (bt - 1)) == 0) continue;
-      if (kept >> p & 1) s_copy[c] = copies++;
-      kept |= 1u << p;
+  const int32_t* table = A.table + (int64_t)row0 * A.stride;
+  // An open block that an earlier row keeps is copied: its parent's, or another
+  // row's that holds the same (beams that begin on one prompt's last block).
+  if (tid < 64) {
+    const int p = tid < W ? s_parent[tid] : -1;
+    const bool open = p >= 0 && (s_len[tid] & (bt - 1)) != 0;
+    const int id = open ? table[p * A.stride + s_blocks[tid] - 1] : -1;
+    const bool known = (unsigned)id < (unsigned)A.num_blocks;
+    bool again = false;
+    for (int o = 0; o < W; ++o) {
+      const int other = __shfl(open ? p : -1, o), other_id = __shfl(id, o);
+      again = again || (open && o < tid && (other == p || (known && other_id == id)));
     }
-    s_copies = copies;
+    const uint64_t mask = __ballot(again);
+    if (tid < W) s_copy[tid] = again ? __popcll(mask & ((1ull << tid) - 1)) : -1;
+    if (tid == 0) s_copies = __popcll(mask);
   }
   __syncthreads();
 
@@ -96,7 +101,6 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
   uint32_t parents = 0;  // old rows that go on
   for (int c = 0; c < W; ++c)
     if (s_parent[c] >= 0) parents |= 1u << s_parent[c];
-  const int32_t* table = A.table + (int64_t)row0 * A.stride;
   int freed = 0;
   for (int j0 = 0; j0 < A.width; j0 += kThreads) {
     const int j = j0 + tid;

@@ -105,8 +105,8 @@ lora_status_t lora_beam_moves_init(void* buf, size_t bytes, int32_t max_rows, in
  * table row parent[c] up to the blocks of its kv_len cached tokens, -1 from
  * there to table_width; new_len[c] = kv_len[parent[c]].
  * Blocks are shared by rows, except a block that is not full and would be
- * written to by several: of the rows with one parent the first keeps such a
- * block, each other takes the next of free_blocks (in the order of rows) and
+ * written to by several: of the rows whose last block is the same the first
+ * keeps it, each other takes the next of free_blocks (in the order of rows) and
  * is listed in moves for lora_beam_copy.
  * Blocks of the old rows that no new row of the request holds are listed in
  * moves->freed, each once, in the order of requests, table columns and rows.

@@ -58,7 +58,7 @@ def reorder(parent, W, kv_len, table, free, num_blocks, bt):
         flags |= 4
     for b in range(R // W):
         rows = range(b * W, (b + 1) * W)
-        heirs = []
+        heirs, opens = [], []
         for c in rows:
             p = int(parent[c])
             if p != -1 and p not in rows:
@@ -69,7 +69,8 @@ def reorder(parent, W, kv_len, table, free, num_blocks, bt):
             blocks = -(-n // bt)
             new_len[c] = n
             new[c, :blocks] = table[p, :blocks]
-            if p in heirs and n % bt:
+            mine = int(table[p, blocks - 1]) if n % bt else -1
+            if n % bt and (p in heirs or (0 <= mine < num_blocks and mine in opens)):
                 at = len(copies)
                 target = int(free[at]) if at < len(free) else -1
                 if at >= len(free):
@@ -79,6 +80,7 @@ def reorder(parent, W, kv_len, table, free, num_blocks, bt):
                 copies.append((int(table[p, blocks - 1]), target, n % bt))
                 new[c, blocks - 1] = target
             heirs.append(p)
+            opens.append(mine)
         held = {(j, int(table[p, j])) for p in heirs for j in range(-(-int(old_len[p]) // bt))}
         last = max(-(-int(old_len[r]) // bt) for r in rows)
         for j in range(last):

@@ -302,6 +302,24 @@ def test_reorder_of_rows_of_different_lengths_and_empty_requests():
         assert r.check()["flags"] == 0
 
 
+@pytest.mark.parametrize("W,bt,prompt", [(2, 16, 5), (4, 16, 40), (8, 64, 100), (32, 128, 200), (3, 16, 32)])
+def test_beams_on_one_prompts_open_block_part(W, bt, prompt):
+    """All rows begin with the prompt's blocks, the last of them among these, and go on from different parents."""
+    rng = np.random.default_rng(W)
+    B, blocks = 2, -(-prompt // bt)
+    ids = rng.permutation(B * blocks + B * W + 2)
+    table = np.full((B * W, blocks + 1), -1)
+    table[:, :blocks] = np.repeat(ids[:B * blocks].reshape(B, blocks), W, 0)
+    base = np.arange(B)[:, None] * W
+    for parent in (np.arange(W) + np.zeros((B, 1), int), np.arange(W)[::-1] + np.zeros((B, 1), int), rng.integers(0, W, (B, W))):
+        r = Reorder((parent + base).flatten(), W, np.full(B * W, prompt), table, ids[B * blocks:], len(ids), bt)
+        r.run()
+        want = r.check()
+        assert want["flags"] == 0 and not want["freed"] and len(want["copies"]) == (B * (W - 1) if prompt % bt else 0)
+        last = r.new.cpu().numpy()[:, blocks - 1]
+        assert not prompt % bt or len(set(last)) == B * W  # every row writes to a block of its own
+
+
 @pytest.mark.parametrize("case", ["parent", "length", "free", "free_id", "table_id", "no_free"])
 def test_reorder_flags(case):
     rng = np.random.default_rng(5)
