@@ -12,7 +12,9 @@ namespace beam {
 
 constexpr int kChunk = 2048;  // logits that a wave holds at once, 32 per lane
 // Waves that a selection's rows are cut into, where the vocabulary has as many
-// chunks.
+// chunks: a wave's first chunk fills its list, so fewer waves insert less, until
+// too few are left to hide latency (64 rows x 8 of 128000 bf16 logits and 128 x 16
+// of 32000, one form of the kernel: 4096 waves 34 and 40 us, 8192 39 and 46).
 constexpr int kTargetWaves = 4096;
 
 // Chunks of a row: its first logit may lie anywhere in a 16-byte vector.

@@ -12,11 +12,11 @@
 //
 // Measured on MI355X (rows, then picks): 64 requests of 8 beams, 128000 bf16
 // logits, 32 + 8 us, 4.1 TB/s of logits; without looking for candidates the
-// rows' launch takes 22.5, 5.8 TB/s (the read rate), so what bounds it is the
+// rows' launch takes 23, 5.6 TB/s (the read rate is 6.1), so what bounds it is the
 // comparisons and insertions of the chunks that follow a wave's first. Fewer,
-// longer waves look less (4096 waves 32 us, 8192 38); waves that tell one another
+// longer waves look less (kTargetWaves); waves that tell one another
 // their lowest kept logit gain nothing, as they keep pace. 128 x 16 of 32000 38 + 8 us;
-// 32 x 5 of 50257 fp32 10 + 11; 1 x 4 of 32000 6.8 + 5.4, latency.
+// 32 x 5 of 50257 fp32 11 + 11; 1 x 4 of 32000 6.8 + 5.4, latency.
 #include <type_traits>
 
 #include "lora_beam_args.h"

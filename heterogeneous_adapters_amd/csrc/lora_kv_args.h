@@ -75,7 +75,8 @@ struct ShareArgs {
   int4 *group_parts, *seq_parts, *items;
 };
 
-// Items of one list of a shared plan, or (list < 0) the join of their results.
+// Items of one list of a shared plan, or of lists 0 and 1 in one launch; the
+// join of their results.
 struct SharedArgs : AttendArgs {
   static constexpr bool kShared = true;
   const int32_t* share;

@@ -14,11 +14,11 @@
 // chunks in one place).
 //
 // Measured on MI355X (attention alone, and lora_kv_attend's time for the same):
-// 256 requests behind 32768 tokens, 32 heads on 8 of 128, 153 us (881): prefix
-// 138 us, 990 TFLOP/s, rests 23, join 9. 96 requests behind 8 prompts of 256 to
-// 4096, 32/32 heads, 48 us (121), 4.4 TB/s. 48 requests, 6 prompts, 15.6 (15.8).
-// Four chunks of 512 tokens among 32 requests behind 3000 and 6000: 245 (243):
-// rows of one chunk share their keys without this.
+// 256 requests behind 32768 tokens, 32 heads on 8 of 128, 157 us (897): of the
+// three launches' times in a trace, prefix 149, rests 24, join 9. 96 requests
+// behind 8 prompts of 256 to 4096, 32/32 heads, 49 us (123), 4.4 TB/s. 48 requests,
+// 6 prompts, 15.0 (16.1). Four chunks of 512 tokens among 32 requests behind 3000
+// and 6000: 249 (247): rows of one chunk share their keys without this.
 #include <utility>
 
 #include "lora_kv_scan.h"
@@ -243,15 +243,17 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
 // between the softmax of another: while a wave's weights of tile t are formed,
 // the matrix unit has the weights of tile t-1 times V and S of tile t+1.
 //
-// 1024 rows on 32768 keys, 8 kv heads of 128: 138 us, 990 TFLOP/s of the 1391
-// that the installed library's 8192^3 product reaches on the same card. Bound by
+// 1024 rows on 32768 keys, 8 kv heads of 128: median of 20 launches 149 us, least
+// 137, 922 and 1000 TFLOP/s; the installed library's 8192^3 product reaches 1367 on
+// the same card. Bound by
 // issue: 32 products take 1024 cycles of a SIMD's matrix unit and hold its vector
 // unit for about 10 cycles each, next to 150 vector instructions (32
-// exponentials of 8.5 cycles among them) of each wave and tile, and the clock is
-// at 1.85 GHz by then. Matrix units are busy for 47 % of the launch. Other ways:
-// four waves that share a conversion 156 us; four waves of 64 rows, one per SIMD,
-// 230 to 270 (spilled); 32 keys at a time with three waves per SIMD 167; every
-// wave converting halves of K and V between its products 142.
+// exponentials of about 9 cycles among them) of each wave and tile, and the clock is
+// at 1.85 GHz by then. Matrix units are busy for 47 % of the launch. Other ways,
+// least of 20 launches as the 137 above: four waves that share a conversion 153
+// us; four waves of 64 rows, one per SIMD, 223 to 265 (spilled); 32 keys at a time
+// with three waves per SIMD 161; every wave converting halves of K and V between
+// its products 143; the requests' kernel of 128 rows 156.
 template <int NC>
 __global__ __launch_bounds__(512, 2) void prefix_kernel(const SharedArgs A) {
   constexpr int D = 32 * NC, kKeys = 64;

@@ -4,8 +4,9 @@ marshalling only.
 Everything between the q/k/v projections and the o projection of a mixed
 multi-LoRA batch: block tables and slot maps (``lora_kv_build``), rotary
 positions (``lora_rope``), the paged 4-bit cache (``lora_kv_append``,
-``lora_kv_gather``), attention over it (``lora_kv_attend``) and over whole
-prompts (``lora_prompt_attend``).  The steps run in liblora.so's HIP kernels;
+``lora_kv_gather``), attention over it (``lora_kv_attend``), over it where
+requests share their first tokens (``lora_kv_share``,
+``lora_kv_attend_shared``) and over whole prompts (``lora_prompt_attend``).  The steps run in liblora.so's HIP kernels;
 this module checks tensors, fills the C structs and raises on a non-zero
 status.  All tensors of a call must be on one GPU; the call runs on that GPU's
 current stream, or on ``stream``.

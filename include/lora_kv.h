@@ -263,8 +263,8 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
  * for up to max_groups groups, built by lora_kv_share after each lora_kv_build
  * and read by every layer's lora_kv_attend_shared.
  * It pays where many rows share much: a decode step's attention of 256 requests
- * behind one prompt of 32768 tokens takes 153 us in place of 881, 96 behind 8
- * prompts of up to 4096 48 in place of 121; 4 beams over a prompt of 1000, or
+ * behind one prompt of 32768 tokens takes 157 us in place of 897, 96 behind 8
+ * prompts of up to 4096 49 in place of 123; 4 beams over a prompt of 1000, or
  * prompts' chunks of hundreds of rows each, take as long either way.  The plan
  * itself, once per step, takes 10 us.
  * Sizes: 0 outside the limits (max_groups in [0, max_seqs]; 2 * max_tokens *
