@@ -35,8 +35,13 @@ constexpr float kLog2eLo = 1.92596299112661746887e-08f;
 constexpr double kLog2e = 1.44269504088896340736, kLn2 = 0.693147180559945309417;
 constexpr float kSlackLogit = 8.0f;
 
-// Logits past this leave fp32's range times log2(e).
-constexpr float kFarLogit = 1e38f;
+// Around references past this the difference to the reference comes first, then
+// its product with log2(e).  Below it r log2(e) rounded to fp32 is off by at
+// most 2^-8, so e^off, which takes that back, by less than 2^-27 after its second
+// power; farther out the three terms do not hold, and from about 2e9 on the
+// weights themselves leave fp32's range.  Every finite logit is right by the
+// difference; ordinary rows never take that way.
+constexpr float kFarLogit = 65536.0f;
 
 // Floats as integers of the same order; 0 is below every one that stands for a logit.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -176,7 +181,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
         if (ref > -INFINITY) sum *= exp((double)ref - (double)top);
         ref = top;
         less = ref * kLog2eHi;
-        const double off = ((double)less - (double)ref * kLog2e) * kLn2;  // 2^-24 of it: e^off by its first terms
+        const double off = ((double)less - (double)ref * kLog2e) * kLn2;  // see kFarLogit: e^off by its first terms
         by = 1.0 + off * (1.0 + 0.5 * off);
       }
       s = 0.0f;
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const SelectArgs A) {
     const double sum0 = sum, by0 = by;
     const float ref0 = ref, less0 = less;
     weigh(std::false_type());
-    // A NaN, an infinity or a logit that is far shows in the sum or the highest.
+    // A NaN or an infinity shows in the sum or the highest, what is far in the reference.
     if (__any(!(s == s)) || !(fabsf(ref) < kFarLogit)) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
