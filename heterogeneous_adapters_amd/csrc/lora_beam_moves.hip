@@ -73,15 +73,18 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const ReorderArgs A) 
   const int32_t* table = A.table + (int64_t)row0 * A.stride;
   // An open block that an earlier row keeps is copied: its parent's, or another
   // row's that holds the same (beams that begin on one prompt's last block).
+  // One that is missing (-1) stays missing in every heir's row: a block of the
+  // free list in its place would pass its last owner's tokens for the beam's.
   if (tid < 64) {
     const int p = tid < W ? s_parent[tid] : -1;
     const bool open = p >= 0 && (s_len[tid] & (bt - 1)) != 0;
     const int id = open ? table[p * A.stride + s_blocks[tid] - 1] : -1;
-    const bool known = (unsigned)id < (unsigned)A.num_blocks;
+    const bool known = (unsigned)id < (unsigned)A.num_blocks, there = open && id != -1;
+    if (open && !known) flags |= LORA_BEAM_FLAG_BLOCK_RANGE;
     bool again = false;
     for (int o = 0; o < W; ++o) {
       const int other = __shfl(open ? p : -1, o), other_id = __shfl(id, o);
-      again = again || (open && o < tid && (other == p || (known && other_id == id)));
+      again = again || (there && o < tid && (other == p || (known && other_id == id)));
     }
     const uint64_t mask = __ballot(again);
     if (tid < W) s_copy[tid] = again ? __popcll(mask & ((1ull << tid) - 1)) : -1;
@@ -179,6 +182,7 @@ __global__ __launch_bounds__(kThreads) void no_moves_kernel(const ReorderArgs A)
 }
 
 // A wave per (copy, layer, kv head): the head's records of a block lie together.
+// What has no source in the cache becomes zeros.
 __global__ __launch_bounds__(256) void copy_kernel(const CopyArgs A) {
   const int lane = threadIdx.x & 63;
   const int copies = min(max(A.counts[LORA_BEAM_COUNT_COPIES], 0), A.max_rows);
@@ -186,11 +190,15 @@ __global__ __launch_bounds__(256) void copy_kernel(const CopyArgs A) {
   for (int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); task < tasks; task += waves) {
     const int h = (int)(task % A.heads), l = (int)(task / A.heads % A.layers), i = (int)(task / A.heads / A.layers);
     const int source = A.source[i], target = A.target[i], units = min((A.tokens[i] + kUnit - 1) / kUnit, A.units);
-    if ((unsigned)source >= (unsigned)A.num_blocks || (unsigned)target >= (unsigned)A.num_blocks) continue;
+    if ((unsigned)target >= (unsigned)A.num_blocks) continue;
     const int64_t head = (int64_t)h * A.units * A.record;
-    const u32x4* from = reinterpret_cast<const u32x4*>(A.base[l] + source * A.stride + head);
     u32x4* to = reinterpret_cast<u32x4*>(A.base[l] + target * A.stride + head);
     const int n = units * A.record / 16;
+    if ((unsigned)source >= (unsigned)A.num_blocks) {
+      for (int k = lane; k < n; k += 64) to[k] = u32x4{0, 0, 0, 0};
+      continue;
+    }
+    const u32x4* from = reinterpret_cast<const u32x4*>(A.base[l] + source * A.stride + head);
     for (int k = lane; k < n; k += 256) {
       u32x4 x[4];
 #pragma unroll

@@ -44,7 +44,7 @@ typedef struct {
 #define LORA_BEAM_FLAG_PARENT 2      /* a parent outside its request (the row is left empty) */
 #define LORA_BEAM_FLAG_LENGTH 4      /* a negative length, or one past the table's row (cut) */
 #define LORA_BEAM_FLAG_FREE_LIST 8   /* the free list ran out (the block's entry is -1) */
-#define LORA_BEAM_FLAG_BLOCK_RANGE 16 /* a block id outside the cache (-1 in its place; not given back) */
+#define LORA_BEAM_FLAG_BLOCK_RANGE 16 /* a block id outside the cache (-1 in its place; not given back), or an open block that is missing */
 
 /* The `beams` best continuations of each request.  Row r with logits x (row r
  * of `logits`, row_stride elements apart, any alignment of its type) offers
@@ -107,7 +107,9 @@ lora_status_t lora_beam_moves_init(void* buf, size_t bytes, int32_t max_rows, in
  * Blocks are shared by rows, except a block that is not full and would be
  * written to by several: of the rows whose last block is the same the first
  * keeps it, each other takes the next of free_blocks (in the order of rows) and
- * is listed in moves for lora_beam_copy.
+ * is listed in moves for lora_beam_copy.  Where a parent's open block is missing
+ * (-1: an earlier step's free list ran out) it is missing in every heir's row
+ * too, nothing is taken or listed for it, and LORA_BEAM_FLAG_BLOCK_RANGE is set.
  * Blocks of the old rows that no new row of the request holds are listed in
  * moves->freed, each once, in the order of requests, table columns and rows.
  * A block is taken to be shared only among the rows of one request at the same
@@ -127,7 +129,9 @@ lora_status_t lora_beam_reorder(const int32_t* parent, const int32_t* kv_len, in
 
 /* The copies of lora_beam_reorder in num_layers caches (host array) of one
  * geometry: whole records of 16 tokens, as many as hold the copy's tokens.
- * Copies whose target is -1, or with a block outside a cache, are left out.
+ * Copies whose target is -1 or outside a cache are left out; where the source
+ * is outside, the target's records are cleared (the values 0), so that nothing
+ * of the block's last owner is attended to.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
 lora_status_t lora_beam_copy(const lora_beam_moves_t* moves, const lora_kv_cache_t* caches, int32_t num_layers,
                              void* stream);
