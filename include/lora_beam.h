@@ -44,7 +44,7 @@ typedef struct {
 #define LORA_BEAM_FLAG_PARENT 2      /* a parent outside its request (the row is left empty) */
 #define LORA_BEAM_FLAG_LENGTH 4      /* a negative length, or one past the table's row (cut) */
 #define LORA_BEAM_FLAG_FREE_LIST 8   /* the free list ran out (the block's entry is -1) */
-#define LORA_BEAM_FLAG_BLOCK_RANGE 16 /* a block id outside the cache (-1 in its place; not given back), or an open block that is missing */
+#define LORA_BEAM_FLAG_BLOCK_RANGE 16 /* an id outside the cache (of the free list: -1 in its place), an open block missing */
 
 /* The `beams` best continuations of each request.  Row r with logits x (row r
  * of `logits`, row_stride elements apart, any alignment of its type) offers
@@ -110,6 +110,8 @@ lora_status_t lora_beam_moves_init(void* buf, size_t bytes, int32_t max_rows, in
  * is listed in moves for lora_beam_copy.  Where a parent's open block is missing
  * (-1: an earlier step's free list ran out) it is missing in every heir's row
  * too, nothing is taken or listed for it, and LORA_BEAM_FLAG_BLOCK_RANGE is set.
+ * Ids of a row outside the cache, other than -1, set it too; they are taken
+ * over as they are (the attention leaves such blocks out) and not given back.
  * Blocks of the old rows that no new row of the request holds are listed in
  * moves->freed, each once, in the order of requests, table columns and rows.
  * A block is taken to be shared only among the rows of one request at the same
