@@ -56,6 +56,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
   const int tid = threadIdx.x, wg = blockIdx.x, nwg = gridDim.x;
   const int bt = 1 << A.bt_log2;
   const int cap = (int)min((int64_t)A.width << A.bt_log2, (int64_t)0x7fffffff);
+  const uint32_t builds = wg == 0 && tid == kCountBuild ? (uint32_t)A.counts[kCountBuild] : 0;  // read ahead of its use
 
   // Tokens per work item, from the cached tokens that all row tiles read.
   const bool many = many_rows(A.T, A.B);
@@ -251,6 +252,7 @@ __global__ __launch_bounds__(kThreads) void build_kernel(const BuildArgs A) {
       if (tid == kCountB) v = A.B;
       if (tid == kCountT) v = A.T;
       if (tid == kCountCheck) v = check_word(A.B, A.T, (int)items0[0], (int)items0[1], (int)items0[2], (int)min(parts0, (int64_t)0x7fffffff));
+      if (tid == kCountBuild) v = (int)(builds + 1);
       A.counts[tid] = v;
     }
     if (tid == kThreads - 1) A.q_indptr[A.B] = used;

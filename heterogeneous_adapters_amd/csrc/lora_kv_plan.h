@@ -21,6 +21,7 @@ constexpr int kTargetWide = 512;
 
 constexpr int kCountTokens = 0, kCountNewBlocks = 1, kCountItems = 2, kCountParts = 3, kCountChunk = 4,
               kCountMid = 5, kCountWide = 6, kCountChunkWide = 7, kCountFlags = 8, kCountB = 9, kCountT = 10, kCountCheck = 11,
+              kCountBuild = 12,  // builds of the buffer so far, by which a shared plan knows its own
               kNumCounts = 16;
 
 // Work items by class of their request's rows (new tokens x query heads per
@@ -102,7 +103,7 @@ constexpr int kLists = 4;      // a shared plan's lists: 0 the groups' prefixes,
 constexpr int kShareItem = 3;  // int4 per item
 LORA_KV_HD inline int min_prefix_chunk(int cls) { return cls == 0 ? 512 : 256; }  // smallest chunk of a prefix
 // counts of a shared plan: kLists item counts, then
-constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShareCheck = 8, kNumShare = 16;
+constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShareCheck = 8, kShareBuild = 9, kNumShare = 16;
 
 // Rows of a prefix's item, as a class, by the groups' average (the host's
 // arithmetic; sizes of single groups and prefixes are known to the device

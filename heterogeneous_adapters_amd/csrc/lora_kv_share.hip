@@ -232,6 +232,7 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
     s[kShareRows] = (int)min(rows0, (int64_t)0x7fffffff);
     s[kShareGroups] = A.groups, s[kShareB] = A.B, s[kShareT] = A.T;
     s[kShareCheck] = share_word(s);
+    s[kShareBuild] = c[kCountBuild];
     for (int i = 0; i < kNumShare; ++i) A.share[i] = s[i];
   }
 }
@@ -547,12 +548,7 @@ __global__ __launch_bounds__(256) void join_kernel(const SharedArgs A, int vecs)
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const int4 p = A.seq_parts[2 * seq + side];  // first result's row, chunks, first token row, rows
-      const int row = ((int)t - p.z) * A.G + hg;
-      // a batch built again after its shared plan
-      if (p.y > 0 && ((int)t < p.z || row >= p.w)) {
-        if (d == 0 && hg == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
-        continue;
-      }
+      const int row = ((int)t - p.z) * A.G + hg;  // one of p.w: rows and plan are of one build
       for (int c0 = grp; c0 < p.y; c0 += kBatch * kGroups) {
         float2 ml[kBatch];
         f4 o[kBatch];

@@ -394,7 +394,8 @@ def lora_kv_share(group_indptr: torch.Tensor, shared_len: torch.Tensor, batch: B
 
 def lora_kv_attend_shared(q: torch.Tensor, out: torch.Tensor, batch: Batch, shared: Shared, block_table: torch.Tensor,
                           cache: Cache, scale: float, ws: torch.Tensor, stream=None) -> None:
-    """lora_kv_attend, with the tokens that groups share attended to together."""
+    """lora_kv_attend, with the tokens that groups share attended to together, by
+    the plan that lora_kv_share made of the batch's last build."""
     (table, stride, width), dtype = _table(block_table), q.dtype
     if block_table.shape[0] != batch.B:
         raise ValueError(f"block_table has {block_table.shape[0]} rows, not {batch.B}")

@@ -123,7 +123,7 @@ typedef struct {
 #define LORA_KV_FLAG_FREE_LIST 4  /* the free list ran out (slots of the rest are -1) */
 #define LORA_KV_FLAG_BLOCK_RANGE 8 /* a block id outside the cache (slot -1; not attended) */
 #define LORA_KV_FLAG_NONFINITE 16 /* lora_kv_append saw an infinity or NaN in K or V */
-#define LORA_KV_FLAG_BATCH 32     /* the batch, or its shared plan, was not built for this call's T and B */
+#define LORA_KV_FLAG_BATCH 32     /* the batch, or its shared plan, was not built for this call */
 #define LORA_KV_FLAG_GROUPS 64    /* lora_kv_share: a group outside the requests, or a negative length (not shared) */
 
 /* Bytes of the buffer (0 outside the limits: max_tokens in [0,
@@ -301,8 +301,8 @@ lora_status_t lora_kv_share(const int32_t* group_indptr, const int32_t* shared_l
  * but for the order of its sums.  num_groups: that of lora_kv_share.
  * ws: device, lora_kv_share_workspace_size(batch, share) bytes, 16-byte
  * aligned, for partial results: calls that share it must not run at the same
- * time.  A plan that was not built for this call's T, B and num_groups writes
- * nothing (LORA_KV_FLAG_BATCH).
+ * time.  A plan that was not built for this call's T, B and num_groups, or whose
+ * batch was built again since, writes nothing (LORA_KV_FLAG_BATCH).
  * Errors: as lora_kv_attend. */
 size_t lora_kv_share_workspace_size(const lora_kv_batch_t* batch, const lora_kv_share_t* share);
 lora_status_t lora_kv_attend_shared(const lora_heads_t* q, const lora_heads_t* o, int32_t T, int32_t B,
