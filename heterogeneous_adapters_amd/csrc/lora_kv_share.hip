@@ -527,7 +527,14 @@ __global__ __launch_bounds__(256) void join_kernel(const SharedArgs A, int vecs)
   typedef typename E::T T;
   constexpr int kBatch = 4, kTasks = 256 / kGroups;  // results in flight; tasks of a work-group
   __shared__ float s_part[kGroups > 1 ? 256 : 1][6];
-  if (!share_ok(A)) return;  // the lists' launches have flagged it
+  const bool ok = share_ok(A), last_build = A.share[kShareBuild] == A.counts[kCountBuild];
+  // Another call's plan, which the lists' launches have flagged; or one of an
+  // earlier build, whose results lie within the workspace all the same: asked
+  // here alone, of the batch's buffer that this launch reads anyway.
+  if (!ok || !last_build) {
+    if (ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&A.counts[kCountFlags], LORA_KV_FLAG_BATCH);
+    return;
+  }
   const int D = vecs * 4, hkv = A.cache.heads, hq = hkv * A.G;
   const int grp = threadIdx.x / kTasks;
   const int64_t task = (int64_t)blockIdx.x * kTasks + threadIdx.x % kTasks;

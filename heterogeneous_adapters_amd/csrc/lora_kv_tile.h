@@ -80,11 +80,11 @@ __device__ __forceinline__ bool plan_ok(const AttendArgs& A) {
          c[kCountWide] <= A.item_cap;
 }
 
-// Whether the shared plan was built for this call and from the batch's last build.
+// Whether the shared plan was built for this call.
 __device__ __forceinline__ bool share_ok(const SharedArgs& A) {
   const int32_t* c = A.share;
   return c[kShareCheck] == share_word(c) && c[kShareB] == A.B && c[kShareT] == A.T && c[kShareGroups] == A.groups &&
-         c[kShareBuild] == A.counts[kCountBuild] && c[kShareRows] <= A.row_cap && max(max(c[0], c[1]), max(c[2], c[3])) <= A.item_cap;
+         c[kShareRows] <= A.row_cap && max(max(c[0], c[1]), max(c[2], c[3])) <= A.item_cap;
 }
 
 // A work item: its request, rows and keys.
