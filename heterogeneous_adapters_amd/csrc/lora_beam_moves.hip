@@ -7,10 +7,13 @@
 // entries of the lists begin depends on the requests before it (one for one
 // request).  The copies are bound by HBM.
 //
-// Measured on MI355X: one request of 4 beams 5.9 us, and 3.8 for the copies in 4
-// layers; 96 requests of 8 beams, up to 2300 tokens in blocks of 64, 5.4 + 10, and
-// 13.6 for 90 MB of copies (read and written). With loops over 32 rows whatever
-// the request's, 10 and 10 + 13 us.
+// Measured on MI355X: one request of 4 beams 6.1 us, and 3.5 for the copies in 4
+// layers; 96 requests of 8 beams, up to 2300 tokens in blocks of 64, 5.9 + 10.4, and
+// 13.4 for 88 MB of copies (read and written).  With loops over 32 rows whatever
+// the request's, 10 and 10 + 13 us.  The loops compare every two rows of a
+// request in straight code, whose masks spill to vector registers: 118 scalars
+// with 16 beams, 245 with 32 (48 requests of 16 beams 29 us for both launches, 24 of
+// 32 70, one of 32 42).
 #include "lora_beam_args.h"
 #include "lora_kv_dev.h"
 

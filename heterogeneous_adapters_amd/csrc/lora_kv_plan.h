@@ -107,12 +107,21 @@ constexpr int kShareRows = 4, kShareGroups = 5, kShareB = 6, kShareT = 7, kShare
 
 // Rows of a prefix's item, as a class, by the groups' average (the host's
 // arithmetic; sizes of single groups and prefixes are known to the device
-// only). Few rows: items of 16, which go with the requests' rests in one launch
-// and read the prefix again from the caches for every 16 rows. More: class 3, or
-// 2 where 256 rows' registers do not suffice. Prefixes of 4000 and 16384, 32 heads on
-// 8 of 128, in 16-row items and else: 240 rows 19 (2000) and 44 us, 34 (2000)
-// and 45; 320 rows 29 and 62, 38 and 57; 512 rows 34 and 74, 41 and 62; 1024 rows
-// 51 and 128, 52 and 94. 200 rows of 256 dims: 63 and 54 us.
+// only).  Few rows: items of 16, which go with the requests' rests in one launch
+// and read the prefix again from the caches for every 16 rows.  More: class 3, or
+// 2 where 256 rows' registers do not suffice.  Attention alone in us, one group,
+// 32 query heads on 8, items of 16 rows / else:
+//   dims  rows  behind 1000     2000     4000     8000     16384 tokens
+//    128   240      17 / 29  20 / 31  26 / 35  31 / 40   44 /  46
+//          320      18 / 30  22 / 34  29 / 38  37 / 43   60 /  57
+//          512      22 / 34  28 / 38  34 / 42  47 / 48   74 /  62
+//         1024      33 / 42  39 / 46  51 / 53  78 / 66  131 /  96
+//    256   100      21 / 33           33 / 39            65 /  62
+//          200      26 / 36           50 / 45           112 /  89
+//          400      41 / 47           71 / 74           160 / 131
+// Where it turns depends on the prefix as well, which the rule does not see.  It
+// goes by the long ones, behind which the other form costs most: 321 to 1024
+// rows behind 4000 tokens or fewer take 1 to 12 us longer than in items of 16.
 constexpr int kFewRows = 320, kFewRowsFar = 128;  // up to 128 dims, and past them
 LORA_KV_HD inline int prefix_class(int64_t T, int64_t G, int64_t groups, int head_dim) {
   return T * G <= (head_dim > 128 ? kFewRowsFar : kFewRows) * groups ? 0 : head_dim > 128 ? 2 : 3;

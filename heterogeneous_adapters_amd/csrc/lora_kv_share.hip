@@ -14,11 +14,20 @@
 // chunks in one place).
 //
 // Measured on MI355X (attention alone, and lora_kv_attend's time for the same):
-// 256 requests behind 32768 tokens, 32 heads on 8 of 128, 157 us (897): of the
-// three launches' times in a trace, prefix 149, rests 24, join 9. 96 requests
-// behind 8 prompts of 256 to 4096, 32/32 heads, 49 us (123), 4.4 TB/s. 48 requests,
-// 6 prompts, 15.0 (16.1). Four chunks of 512 tokens among 32 requests behind 3000
-// and 6000: 249 (247): rows of one chunk share their keys without this.
+// 256 requests behind 32768 tokens, 32 heads on 8 of 128, 155 us (889): of the
+// three launches' times in a trace, prefix 141, rests 24, join 10.  96 requests
+// behind 8 prompts of 256 to 4096, 32/32 heads, 49 us (123), 4.4 TB/s.  48 requests,
+// 6 prompts, 15.5 (16.1).  4 beams over 1000 tokens 11.6 (10.4).  Four chunks of 512
+// tokens among 32 requests behind 3000 and 6000: 246 (245): rows of one chunk
+// share their keys without this.
+// 256 requests behind 8192 tokens (floor: products at the library's rate, in
+// fp32 three times as many): 76 us (259), floor 25; of 256 dims 179 (630), floor 50;
+// fp32 194 (423), floor 74, since its tiles of 32 rows convert the prefix each.
+//
+// Weights are rounded to bf16 for their product with V, in both parts, and the
+// sums are of the rounded weights, as in lora_kv_attend: bf16 results are off by
+// 0.0018 to 0.0022 of their size, of which 0.0017 is their own rounding.  fp32 keeps
+// 24 bits of queries and weights, and partial results are fp32 in either.
 #include <utility>
 
 #include "lora_kv_scan.h"
@@ -53,7 +62,7 @@ struct Entry {
   int list, seq, qs, rows, pos0, kv, base, chunk, group;
 };
 
-// One work-group: integer work on a few kilobytes per step, 9 to 11 us of
+// One work-group: integer work on a few kilobytes per step, 9 to 12 us of
 // dependent reads (counters and lengths, positions, results of groups for
 // their requests) and sums between barriers. Groups' bounds lie in LDS, and a
 // request's numbers in its thread's registers, where there are few enough.
@@ -244,13 +253,16 @@ __global__ __launch_bounds__(kPlanThreads) void share_kernel(const ShareArgs A) 
 // between the softmax of another: while a wave's weights of tile t are formed,
 // the matrix unit has the weights of tile t-1 times V and S of tile t+1.
 //
-// 1024 rows on 32768 keys, 8 kv heads of 128: median of 20 launches 149 us, least
-// 137, 922 and 1000 TFLOP/s; the installed library's 8192^3 product reaches 1367 on
-// the same card. Bound by
-// issue: 32 products take 1024 cycles of a SIMD's matrix unit and hold its vector
-// unit for about 10 cycles each, next to 150 vector instructions (32
-// exponentials of about 9 cycles among them) of each wave and tile, and the clock is
-// at 1.85 GHz by then. Matrix units are busy for 47 % of the launch. Other ways,
+// 1024 rows on 32768 keys, 8 kv heads of 128: median of 20 launches 141 us, least
+// 137, 977 and 1006 TFLOP/s; the installed library's 8192^3 product reaches 1431 on
+// the same card.  No unit is full: matrix units are busy for 47 % of the launch,
+// vector units for 44, LDS for 33, and waves wait for 27 % of their cycles.  Issue
+// alone (38 cycles a product by a probe of the single instructions: a product
+// holds the vector unit for about 10, next to 150 vector instructions of each wave
+// and tile, 32 exponentials of about 9 cycles among them) makes 156000 of its 280000
+// cycles.  The rest goes to the barrier of every tile: registers leave room for
+// one work-group per compute unit, and both waves of a SIMD come out of it in the
+// same phase.  Other ways,
 // least of 20 launches as the 137 above: four waves that share a conversion 153
 // us; four waves of 64 rows, one per SIMD, 223 to 265 (spilled); 32 keys at a time
 // with three waves per SIMD 161; every wave converting halves of K and V between

@@ -7,8 +7,17 @@
  * is row b*beams + w of every array, and of the decode batch (one request of
  * lora_kv_build per beam).  A search's step:
  *   logits -> lora_beam_select -> lora_beam_reorder -> lora_beam_copy
- *   -> lora_kv_build, then per layer lora_kv_append and lora_kv_attend (or
- *   lora_kv_attend_shared: the beams of a request share its prompt).
+ *   -> lora_kv_build, then per layer lora_kv_append and lora_kv_attend.
+ * The beams of a request share its prompt, so lora_kv_attend_shared gives the
+ * same; it is faster where beams and prompts are many and long, and slower for a
+ * few beams over a thousand tokens (lora_kv.h has the figures).
+ *
+ * lora_beam_reorder takes its blocks from the front of the free list, and so
+ * does lora_kv_build: between the two the list's owner drops its first
+ * counts[LORA_BEAM_COUNT_COPIES] ids and may append the
+ * counts[LORA_BEAM_COUNT_FREED] of moves->freed.  With the same list for both two
+ * rows would write to one block, which no flag shows.  The counts are on the
+ * device, so reading them waits for the reorder.
  *
  * The general rules of lora.h hold, as in lora_kv.h: device pointers unless a
  * comment says host, caller-owned buffers, asynchronous enqueue on `stream`,
@@ -35,7 +44,7 @@ extern "C" {
 
 /* State of the beams, one entry per row. */
 typedef struct {
-  float* score;    /* sum of the log-probabilities of its tokens; -inf (or NaN): the row has no beam */
+  float* score;    /* sum of the log-probabilities of its tokens; not finite: the row has no beam */
   int32_t* length; /* generated tokens */
   int32_t* done;   /* not 0: the beam has ended */
 } lora_beams_t;
@@ -54,7 +63,7 @@ typedef struct {
  * the token eos.  Candidates are ranked by total / max(length, 1)^length_penalty
  * (0: by total), the highest first, equal ones by the lower
  * row, then the higher logit, then the lower token.  Sums and ranks are formed in 64 bits (exponentials in
- * 32), from logits of 16 or 32; totals are rounded once, to fp32.
+ * 32), from finite logits of any size, of 16 or 32 bits; totals are rounded once, to fp32.
  * A logit of -inf is never chosen.  Where a request has fewer candidates than
  * beams, the rest of its rows get parent and token -1, score -inf, length 0
  * and done 1.
@@ -107,7 +116,8 @@ lora_status_t lora_beam_moves_init(void* buf, size_t bytes, int32_t max_rows, in
  * Blocks are shared by rows, except a block that is not full and would be
  * written to by several: of the rows whose last block is the same the first
  * keeps it, each other takes the next of free_blocks (in the order of rows) and
- * is listed in moves for lora_beam_copy.  Where a parent's open block is missing
+ * is listed in moves for lora_beam_copy, beams that have ended among them (the
+ * call does not know which).  Where a parent's open block is missing
  * (-1: an earlier step's free list ran out) it is missing in every heir's row
  * too, nothing is taken or listed for it, and LORA_BEAM_FLAG_BLOCK_RANGE is set.
  * Ids of a row outside the cache, other than -1, set it too; they are taken

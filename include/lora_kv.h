@@ -263,10 +263,12 @@ lora_status_t lora_kv_attend(const lora_heads_t* q, const lora_heads_t* o, int32
  * for up to max_groups groups, built by lora_kv_share after each lora_kv_build
  * and read by every layer's lora_kv_attend_shared.
  * It pays where many rows share much: a decode step's attention of 256 requests
- * behind one prompt of 32768 tokens takes 157 us in place of 897, 96 behind 8
- * prompts of up to 4096 49 in place of 123; 4 beams over a prompt of 1000, or
- * prompts' chunks of hundreds of rows each, take as long either way.  The plan
- * itself, once per step, takes 10 us.
+ * behind one prompt of 32768 tokens takes 155 us in place of 889, 96 behind 8
+ * prompts of up to 4096 49 in place of 123, 64 behind 2000 22 in place of 30.  A few
+ * beams over a prompt of 1000, or prompts' chunks of hundreds of rows each, take
+ * as long either way or a little longer (11.6 us against 10.4, 246 against 245),
+ * and the plan itself, once per step, takes 10 us: these are better left to
+ * lora_kv_attend.  No call chooses by itself.
  * Sizes: 0 outside the limits (max_groups in [0, max_seqs]; 2 * max_tokens *
  * query heads per kv head + 2^18 < 2^31, and the work items of
  * lora_kv_batch_size with max_groups more).
