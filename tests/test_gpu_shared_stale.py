@@ -1,4 +1,4 @@
-"""A shared plan belongs to one build of its batch."""
+"""A shared plan belongs to one build of its batch; steps padded to a size."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +78,25 @@ def test_plans_of_two_captured_steps_in_turn():
         graphs[k].replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[k], want[k]) and int(s.batch.flags) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,G,D", [(3, 1, 64), (50, 8, 64), (11, 32, 160)])
+def test_padded_steps_leave_the_rows_behind_alone(n, G, D, dtype):
+    """More rows than the requests bring: a graph's size.  With T past B other classes of items come into play."""
+    s = SharedStep(n, [120 + i for i in range(n)], [1] * n, [0, n], [112], G, 1, D, 16, dtype)
+    s.check(s.run(0.125), 0.125)
+    for pad in (1, 40):
+        T = s.T + pad
+        batch = kv.Batch(T, n, G, 1, D)
+        shared = kv.Shared(batch, 1)
+        ws = kv.shared_workspace(batch, shared)
+        q = torch.full((T, G, D), float("nan"), dtype=s.dq.dtype, device=s.dq.device)
+        q[:s.T] = s.dq
+        out = torch.full_like(q, 3.0)
+        kv.lora_kv_build(i32(s.ctx), i32(s.new), T, s.tab, i32(s.free), s.num, s.bt, batch)
+        kv.lora_kv_share(i32(s.groups), i32(s.lens), batch, shared)
+        kv.lora_kv_attend_shared(q, out, batch, shared, s.tab, s.cache, 0.125, ws)
+        torch.cuda.synchronize()
+        s.check(host(out[:s.T]), 0.125)
+        assert torch.all(out[s.T:] == 3.0) and int(batch.flags) == 0
